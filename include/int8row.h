@@ -142,6 +142,37 @@ i8r_status int8_mixed_linear_wq(const void *X, int T, int K,
                                 cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * int8_mixed_linear_fused: the layer with the work that follows it in a
+ * decoder layer (bias, activation, residual) in its epilogue:
+ *   Y = fp16( act( XW + bias[n] ) + residual[t,n] )
+ * with XW the fp32 value int8_mixed_linear would round, and every step in
+ * fp32 before the one rounding.
+ *
+ *   W16       [K,N] fp16, or null for the Wq-only variant
+ *   bias      [N] fp16, or null for none
+ *   act       I8R_ACT_NONE; I8R_ACT_RELU (max(y, 0), NaN stays NaN);
+ *             I8R_ACT_GELU (y * Phi(y), Phi the normal distribution function)
+ *   residual  [T,N] fp16, or null for none; it may be Y itself (the sum in
+ *             place), and must not overlap Y in any other way
+ * The other arguments, rules and errors are those of int8_mixed_linear (W16
+ * given) or int8_mixed_linear_wq (W16 null), and so is the workspace: the same
+ * size query.  Without bias, activation and residual the result is theirs bit
+ * for bit.  An unknown act returns I8R_EINVAL.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    I8R_ACT_NONE = 0,
+    I8R_ACT_RELU = 1,
+    I8R_ACT_GELU = 2
+} i8r_activation;
+
+i8r_status int8_mixed_linear_fused(const void *X, int T, int K,
+                                   const int8_t *Wq, const float *sW, const void *W16, int N,
+                                   float alpha, const void *bias, i8r_activation act,
+                                   const void *residual, void *Y,
+                                   void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * int8_mixed_linear_chain: several int8_mixed_linear layers run in order on one
  * stream with one shared workspace: the projections of a decoder layer (the
  * pages' unit of use: the Int8 multiplication of the feed-forward and

@@ -14,6 +14,7 @@ __all__ = [
     "lib", "I8RError",
     "int8_quantize_weight_colwise", "int8_mixed_linear_workspace_size", "int8_mixed_linear",
     "int8_mixed_linear_wq_workspace_size", "int8_mixed_linear_wq_max_outliers", "int8_mixed_linear_wq",
+    "int8_mixed_linear_fused",
     "int8_outlier_stats_workspace_size", "int8_outlier_stats", "int8_quantize_activation",
     "int8_gemm_i8_s32", "int8_read_and_clear_device_status", "int8_status_string",
     "int8_selftest_wait_timeout",
@@ -25,6 +26,7 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libint8row.so")
 DECODE_MAX_T = 128
 INT4_MAX_T = 64
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2}        # i8r_activation
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -61,6 +63,7 @@ def lib():
     so.int8_mixed_linear_wq_max_outliers.argtypes = [_I]
     so.int8_mixed_linear_wq_max_outliers.restype = _I
     so.int8_mixed_linear_wq.argtypes = [_P, _I, _I, _P, _P, _I, _F, _P, _P, _Z, _P]
+    so.int8_mixed_linear_fused.argtypes = [_P, _I, _I, _P, _P, _P, _I, _F, _P, _I, _P, _P, _P, _Z, _P]
     so.int8_mixed_linear_chain_workspace_size.argtypes = [_I, _P]
     so.int8_mixed_linear_chain_workspace_size.restype = _Z
     so.int8_mixed_linear_chain.argtypes = [_I, _P, _P, _Z, _P]
@@ -95,7 +98,7 @@ def lib():
     so.int4_linear_workspace_size.argtypes = [_I, _I, _I]
     so.int4_linear_workspace_size.restype = _Z
     so.int4_linear.argtypes = [_P, _I, _I, _P, _P, _I, _P, _P, _Z, _P]
-    for name in ("int8_quantize_weight_colwise", "int8_mixed_linear", "int8_outlier_stats",
+    for name in ("int8_quantize_weight_colwise", "int8_mixed_linear", "int8_mixed_linear_fused", "int8_outlier_stats",
                  "int8_quantize_activation", "int8_gemm_i8_s32", "int8_read_and_clear_device_status",
                  "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear"):
         getattr(so, name).restype = _I
@@ -125,6 +128,39 @@ def _dev(t, dtype, name, ndim=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(first, *rest):
+    """The device of the tensor `first`, which every other tensor given has to be on."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return first.device
+
+
+class _on:
+    """Run with `device` current and allocations made on the stream the call uses, so that a
+    buffer freed at the end of the call is not handed out again before its kernels ran."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._device = torch.cuda.device(device)
+        self._stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        self._device.__exit__(*exc)
 
 
 def int8_quantize_weight_colwise(W16, Wq=None, sW=None, stream=None):
@@ -185,6 +221,38 @@ def int8_mixed_linear_wq(X, Wq, sW, alpha=6.0, Y=None, workspace_buf=None, strea
         _dev(X, torch.float16, "X", 2), T, K, _dev(Wq, torch.int8, "Wq", 2), _dev(sW, torch.float32, "sW"),
         N, float(alpha), _dev(Y, torch.float16, "Y"),
         ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)))
+    return Y
+
+
+def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none", residual=None, Y=None,
+                            workspace_buf=None, stream=None):
+    """Y fp16 [T,N] = act(XW + bias) + residual, XW the LLM.int8() linear of X fp16 [T,K]
+    (W16 None: the Wq-only variant).  bias fp16 [N], residual fp16 [T,N] (may be Y itself),
+    act one of "none", "relu", "gelu"."""
+    import torch
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    x = _dev(X, torch.float16, "X", 2)
+    T, K = X.shape
+    wq = _dev(Wq, torch.int8, "Wq", 2)
+    N = Wq.shape[1]
+    _shape(Wq, (K, N), "Wq")
+    _shape(sW, (N,), "sW")
+    for t, name, shape in ((W16, "W16", (K, N)), (bias, "bias", (N,)), (residual, "residual", (T, N)), (Y, "Y", (T, N))):
+        if t is not None:
+            _shape(t, shape, name)
+    dev = _same_device(X, Wq, sW, W16, bias, residual, Y, workspace_buf)
+    opt = lambda t, name: _dev(t, torch.float16, name) if t is not None else _P()
+    with _on(dev, stream):
+        Y = torch.empty((T, N), dtype=torch.float16, device=dev) if Y is None else Y
+        if workspace_buf is None:
+            size = int8_mixed_linear_wq_workspace_size if W16 is None else int8_mixed_linear_workspace_size
+            workspace_buf = torch.empty(max(1, size(T, K, N)), dtype=torch.uint8, device=dev)
+        ws = workspace_buf
+        _check("int8_mixed_linear_fused", lib().int8_mixed_linear_fused(
+            x, T, K, wq, _dev(sW, torch.float32, "sW"), opt(W16, "W16"), N, float(alpha), opt(bias, "bias"),
+            ACTIVATIONS[act], opt(residual, "residual"), _dev(Y, torch.float16, "Y"),
+            ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)))
     return Y
 
 

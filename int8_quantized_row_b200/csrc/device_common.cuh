@@ -480,4 +480,35 @@ __device__ __forceinline__ float recip127(float absmax) {
     return absmax > 0.0f ? __fdiv_rn(127.0f, absmax) : 0.0f;
 }
 
+// What int8_mixed_linear_fused adds to the dequantised sum y of element (t, n),
+// in fp32, before the one rounding to fp16: y' = act(y + bias[n]) + residual[t,n].
+struct Epilogue {
+    const __half *bias = nullptr;        // [N] fp16 or null
+    const __half *residual = nullptr;    // [T,N] fp16 or null; may be Y itself
+    int act = I8R_ACT_NONE;
+    bool any() const { return bias || residual || act != I8R_ACT_NONE; }
+};
+
+// relu keeps NaN (a comparison, not fmaxf).  gelu is y * Phi(y) with Phi from
+// erfcf, whose relative error stays small in the left tail where 1 + erff
+// cancels.
+__device__ __forceinline__ float activate(float y, int act) {
+    if (act == I8R_ACT_RELU) return y < 0.0f ? 0.0f : y;
+    if (act == I8R_ACT_GELU) return 0.5f * y * erfcf(-0.70710678f * y);
+    return y;
+}
+
+// The epilogue of eight neighbouring columns: b8 and r8 hold eight fp16 of the
+// bias and the residual (zero where the call has none).
+__device__ __forceinline__ void apply_epilogue8(float (&y)[8], const uint4 &b8, const uint4 &r8, int act) {
+    const __half2 *b = reinterpret_cast<const __half2 *>(&b8);
+    const __half2 *r = reinterpret_cast<const __half2 *>(&r8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 bf = __half22float2(b[e]), rf = __half22float2(r[e]);
+        y[2 * e] = activate(y[2 * e] + bf.x, act) + rf.x;
+        y[2 * e + 1] = activate(y[2 * e + 1] + bf.y, act) + rf.y;
+    }
+}
+
 }  // namespace i8r

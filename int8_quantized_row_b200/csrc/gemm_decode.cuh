@@ -88,6 +88,7 @@ struct Params {
     int wq_only;                   // no W16: outlier rows from W16o, dequantised from Wq past o_rows
     int may_outlier;               // alpha < +inf: a tile's first stage may be an outlier stage
     __half *Y;
+    Epilogue epi;                  // decode_finalize_kernel's bias, activation and residual
     float *Yo;                     // [T,N] fp32: the 16-bit outlier part (written when |O| > 0)
 };
 
@@ -147,17 +148,27 @@ __device__ __forceinline__ bool walk_stages(const Params &p, long long u0, long 
 
 // Y from the reduced int32 sums: one thread per 8 columns of a row,
 //   Y[t,n] = fp16( acc32[t,n] * (sX[t] / 127^2) * sW[n] + Yo[t,n] )
-// (one fp32 fma after the scale product); a programmatic dependent of the GEMM.
+// (one fp32 fma after the scale product), with kEpi followed by the fused
+// epilogue (bias, activation, residual; two more reads of at most 2 bytes per
+// element, requested before the GEMM's sums are waited for: neither is written
+// by this call).  A programmatic dependent of the GEMM.
+template <bool kEpi>
 __global__ void __launch_bounds__(256) decode_finalize_kernel(const int32_t *__restrict__ acc32,
                                                               const float *__restrict__ Yo,
                                                               const int32_t *__restrict__ count,
                                                               const float *__restrict__ sX, const float *__restrict__ sW,
-                                                              int T, int N, __half *__restrict__ Y) {
-    griddep_wait();
+                                                              int T, int N, __half *Y, const Epilogue epi) {
+    if (!kEpi) griddep_wait();
     const int groups = N / 8;
     const long long g = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (g >= static_cast<long long>(T) * groups) return;
     const int t = static_cast<int>(g / groups), n = static_cast<int>(g % groups) * 8;
+    uint4 b8 = make_uint4(0u, 0u, 0u, 0u), r8 = b8;
+    if (kEpi) {
+        if (epi.bias) b8 = __ldg(reinterpret_cast<const uint4 *>(epi.bias + n));
+        if (epi.residual) r8 = __ldcg(reinterpret_cast<const uint4 *>(epi.residual + static_cast<size_t>(t) * N + n));
+        griddep_wait();
+    }
     const bool yo = Yo && *count > 0;
     const size_t at = static_cast<size_t>(t) * N + n;
     const int4 a0 = __ldcg(reinterpret_cast<const int4 *>(acc32 + at));
@@ -173,9 +184,13 @@ __global__ void __launch_bounds__(256) decode_finalize_kernel(const int32_t *__r
     const int av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
     const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     const float ov[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+    float yf[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) yf[e] = fmaf(static_cast<float>(av[e]), rs * wv[e], ov[e]);
+    if (kEpi) apply_epilogue8(yf, b8, r8, epi.act);
     __align__(16) __half y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __float2half_rn(fmaf(static_cast<float>(av[e]), rs * wv[e], ov[e]));
+    for (int e = 0; e < 8; ++e) y[e] = __float2half_rn(yf[e]);
     *reinterpret_cast<uint4 *>(Y + at) = *reinterpret_cast<const uint4 *>(y);
 }
 

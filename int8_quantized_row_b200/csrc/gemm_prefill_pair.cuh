@@ -75,6 +75,7 @@ struct Params {
     int o_rows;                    // outlier rows compacted into the W16o map (multiple of 64)
     int wq_only;                   // no W16 map: blocks past o_rows are dequantised from Wq by index
     const int8_t *Wq;              // [K,N] int8 (the Wq-only variant's rows past the compacted ones)
+    Epilogue epi;                  // bias, activation, residual (kEpi instances)
 };
 
 struct Barriers {
@@ -116,7 +117,10 @@ __device__ __forceinline__ bool walk_schedule(const Params &p, int nob, int clus
     return true;
 }
 
-template <bool kS32>
+// kS32: int32 accumulators out.  kEpi: Y with the fused epilogue (bias,
+// activation, residual); its own instance, so that the plain layer's epilogue
+// stays as it is.
+template <bool kS32, bool kEpi>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_prefill_pair_kernel(const __grid_constant__ CUtensorMap map_xq, const __grid_constant__ CUtensorMap map_wq,
                              const __grid_constant__ CUtensorMap map_xo, const __grid_constant__ CUtensorMap map_w16,
@@ -424,6 +428,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 reinterpret_cast<float4 *>(sw_s)[lane * 2 + 1] = s1;
                 __syncwarp();
             }
+            // Fused epilogue: the residual of a 32-column chunk (64 bytes of this
+            // lane's row) and its bias are requested one chunk ahead, the first
+            // chunk's before the accumulator is waited for.
+            uint4 res[4], bia[4];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int n = n0 + c * 32 + g * 8;
+                    res[g] = bia[g] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < p.N && p.epi.bias) bia[g] = __ldg(reinterpret_cast<const uint4 *>(p.epi.bias + n));
+                    if (n < p.N && row_ok && p.epi.residual)
+                        res[g] = __ldcg(reinterpret_cast<const uint4 *>(p.epi.residual + static_cast<size_t>(t) * p.N + n));
+                }
+            };
+            if (kEpi) fetch(0);
             if (!warp_wait(&bars->acc_int_full[buf], use, abort, I8R_DEV_TMEM_TIMEOUT)) break;
             tc_fence_after_sync();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * BN);
@@ -470,22 +489,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(taddr + c * 32, r);
                     tmem_wait_ld();
                     uint4 out[4];
+                    uint4 res_now[4], bia_now[4];
+                    if (kEpi) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) res_now[g] = res[g], bia_now[g] = bia[g];
+                        if (c + 1 < BN / 32) fetch(c + 1);
+                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = g * 8 + e;
+                            y[e] = nob ? __uint_as_float(r[i])
+                                       : static_cast<float>(static_cast<int>(r[i])) * (rs * sw_s[c * 32 + i]);
+                        }
+                        if (kEpi) apply_epilogue8(y, bia_now[g], res_now[g], p.epi.act);
                         __half2 h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i0 = g * 8 + 2 * e, i1 = i0 + 1;
-                            float y0, y1;
-                            if (nob) {
-                                y0 = __uint_as_float(r[i0]);
-                                y1 = __uint_as_float(r[i1]);
-                            } else {
-                                y0 = static_cast<float>(static_cast<int>(r[i0])) * (rs * sw_s[c * 32 + i0]);
-                                y1 = static_cast<float>(static_cast<int>(r[i1])) * (rs * sw_s[c * 32 + i1]);
-                            }
-                            h[e] = __floats2half2_rn(y0, y1);
-                        }
+                        for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
                         out[g] = *reinterpret_cast<uint4 *>(h);
                     }
                     uint8_t *blk = stage_s + (chunk_seq & 1) * EPI_STAGE_BYTES;

@@ -149,10 +149,13 @@ i8r_status device_setup(const DeviceInfo **out) {
         I8R_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
         d.sm100 = (major == 10 && minor == 0);
         if (d.sm100) {
-            I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<false>,
+            I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<false, false>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(prefill2::SMEM_BYTES)));
-            I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<true>,
+            I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<false, true>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(prefill2::SMEM_BYTES)));
+            I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<true, false>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(prefill2::SMEM_BYTES)));
             cudaLaunchConfig_t cfg = {};
@@ -166,7 +169,7 @@ i8r_status device_setup(const DeviceInfo **out) {
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            I8R_CUDA(cudaOccupancyMaxActiveClusters(&d.pair_clusters, prefill2::gemm_prefill_pair_kernel<false>, &cfg));
+            I8R_CUDA(cudaOccupancyMaxActiveClusters(&d.pair_clusters, prefill2::gemm_prefill_pair_kernel<false, false>, &cfg));
             if (d.pair_clusters < 1) return I8R_EARCH;
             I8R_CUDA(cudaFuncSetAttribute(decode::gemm_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(decode::SMEM_MAX)));
@@ -507,7 +510,7 @@ void record_after(cudaStream_t s) {
 i8r_status launch_prefill(const DeviceInfo *dev, const int8_t *Xq, const __half *Xo, int T, int K,
                           const int8_t *Wq, const float *sW, const __half *W16, int N, const int32_t *count,
                           const int32_t *idx, const float *sX, __half *Y, int32_t *acc_out, cudaStream_t s,
-                          const __half *W16o = nullptr) {
+                          const __half *W16o = nullptr, const Epilogue &epi = {}) {
     CUtensorMap map_xq, map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y;
     I8R_TRY(make_map(&map_xq, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, T, K, 128, prefill2::A_BOX_K));
     I8R_TRY(make_map(&map_wq, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, prefill2::BK, 128));
@@ -557,15 +560,20 @@ i8r_status launch_prefill(const DeviceInfo *dev, const int8_t *Xq, const __half 
     p.o_rows = o_rows;
     p.wq_only = wq_only ? 1 : 0;
     p.Wq = Wq;
+    p.epi = epi;
     const int clusters = p.num_tiles < dev->pair_clusters ? p.num_tiles : dev->pair_clusters;
     record_before(s);
     cudaError_t e;
-    if (Y)
-        e = launch_dependent(prefill2::gemm_prefill_pair_kernel<false>, dim3(2 * clusters), dim3(prefill2::THREADS),
-                             prefill2::SMEM_BYTES, s, 2, map_xq, map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y, p);
+    auto launch = [&](auto kernel) {
+        return launch_dependent(kernel, dim3(2 * clusters), dim3(prefill2::THREADS), prefill2::SMEM_BYTES, s, 2, map_xq,
+                                map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y, p);
+    };
+    if (!Y)
+        e = launch(prefill2::gemm_prefill_pair_kernel<true, false>);
+    else if (epi.any())
+        e = launch(prefill2::gemm_prefill_pair_kernel<false, true>);
     else
-        e = launch_dependent(prefill2::gemm_prefill_pair_kernel<true>, dim3(2 * clusters), dim3(prefill2::THREADS),
-                             prefill2::SMEM_BYTES, s, 2, map_xq, map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y, p);
+        e = launch(prefill2::gemm_prefill_pair_kernel<false, false>);
     if (e != cudaSuccess) {
         tl_last_cuda_error = static_cast<int>(e);
         return I8R_ECUDA;
@@ -634,9 +642,10 @@ i8r_status launch_decode(const DeviceInfo *dev, const int8_t *Xq, int T, int K, 
     record_after(s);
     if (fin) {
         const long long items = static_cast<long long>(T) * (N / 8);
-        e = launch_dependent(decode::decode_finalize_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256),
-                             0, s, 1, static_cast<const int32_t *>(acc32), static_cast<const float *>(fin->Yo),
-                             fin->count, fin->sX, fin->sW, T, N, fin->Y);
+        e = launch_dependent(fin->epi.any() ? decode::decode_finalize_kernel<true> : decode::decode_finalize_kernel<false>,
+                             dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, s, 1,
+                             static_cast<const int32_t *>(acc32), static_cast<const float *>(fin->Yo), fin->count,
+                             fin->sX, fin->sW, T, N, fin->Y, fin->epi);
         if (e != cudaSuccess) {
             tl_last_cuda_error = static_cast<int>(e);
             return I8R_ECUDA;
@@ -759,10 +768,10 @@ size_t int8_mixed_linear_workspace_size(int T, int K, int N) {
 
 namespace {
 
-// int8_mixed_linear and its Wq-only variant (W16 null).
+// int8_mixed_linear and its Wq-only variant (W16 null), with the fused epilogue.
 i8r_status mixed_linear_impl(const void *X, int T, int K, const int8_t *Wq, const float *sW, const void *W16, int N,
                              float alpha, void *Y, void *workspace, size_t workspace_bytes, cudaStream_t stream,
-                             bool compact_decode = true) {
+                             bool compact_decode = true, const Epilogue &epi = {}) {
     const bool wq_only = W16 == nullptr;
     I8R_TRY(check_shape(T, K, N, true));
     if (std::isnan(alpha) || alpha < 0.0f) return I8R_EINVAL;
@@ -801,7 +810,7 @@ i8r_status mixed_linear_impl(const void *X, int T, int K, const int8_t *Wq, cons
     I8R_TRY(launch_activation(dev, x, T, K, alpha, mask, idx, count, sX, Xq, Xo, small_t ? acc32 : nullptr,
                               zero_bytes, stream, w16, N, W16o, Wq, sW, reinterpret_cast<unsigned *>(ws + w.ctr)));
     if (!small_t)
-        return launch_prefill(dev, Xq, Xo, T, K, Wq, sW, w16, N, count, idx, sX, y, nullptr, stream, W16o);
+        return launch_prefill(dev, Xq, Xo, T, K, Wq, sW, w16, N, count, idx, sX, y, nullptr, stream, W16o, epi);
 
     decode::Params fin{};
     fin.sX = sX;
@@ -813,6 +822,7 @@ i8r_status mixed_linear_impl(const void *X, int T, int K, const int8_t *Wq, cons
     fin.may_outlier = std::isinf(alpha) ? 0 : 1;   // alpha = +inf: no finite input is an outlier
     fin.Y = y;
     fin.Yo = Yo;
+    fin.epi = epi;
     return launch_decode(dev, Xq, T, K, Wq, N, acc32, &fin, stream, Xo, w16, W16o);
 }
 
@@ -834,6 +844,21 @@ int int8_mixed_linear_wq_max_outliers(int K) { return K < 0 ? 0 : compact_rows(K
 i8r_status int8_mixed_linear_wq(const void *X, int T, int K, const int8_t *Wq, const float *sW, int N, float alpha,
                                 void *Y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     return mixed_linear_impl(X, T, K, Wq, sW, nullptr, N, alpha, Y, workspace, workspace_bytes, stream);
+}
+
+i8r_status int8_mixed_linear_fused(const void *X, int T, int K, const int8_t *Wq, const float *sW, const void *W16,
+                                   int N, float alpha, const void *bias, i8r_activation act, const void *residual,
+                                   void *Y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    I8R_TRY(check_shape(T, K, N, true));
+    const int a = static_cast<int>(act);
+    if (a < I8R_ACT_NONE || a > I8R_ACT_GELU) return I8R_EINVAL;
+    if (T > 0 && bias) I8R_TRY(check_ptr(bias));
+    if (T > 0 && residual) I8R_TRY(check_ptr(residual));
+    Epilogue epi;
+    epi.bias = static_cast<const __half *>(bias);
+    epi.residual = static_cast<const __half *>(residual);
+    epi.act = a;
+    return mixed_linear_impl(X, T, K, Wq, sW, W16, N, alpha, Y, workspace, workspace_bytes, stream, true, epi);
 }
 
 size_t int8_mixed_linear_chain_workspace_size(int n, const i8r_layer *layers) {

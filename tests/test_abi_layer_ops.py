@@ -1,0 +1,49 @@
+"""Host-side checks of the decoder layer's operators through the C ABI (CPU only:
+no call here gets as far as the device)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def so():
+    from int8_quantized_row_b200 import build
+    build.build()
+    import int8_quantized_row_b200 as m
+    return m.lib()
+
+
+def p(addr=4096):
+    return ctypes.c_void_p(addr)
+
+
+NULL = ctypes.c_void_p(0)
+OK, EINVAL, EALIGN, ERANGE, EWORKSPACE = 0, 1, 2, 3, 4
+
+
+def test_fused_linear_refusals(so):
+    f = so.int8_mixed_linear_fused
+    size = so.int8_mixed_linear_workspace_size(16, 1024, 1024)
+    size_wq = so.int8_mixed_linear_wq_workspace_size(16, 1024, 1024)
+
+    def call(T=16, K=1024, N=1024, x=p(), w16=p(), alpha=6.0, bias=p(), act=1, res=p(), y=p(), ws=p(), wsb=size):
+        return f(x, T, K, p(), p(), w16, N, alpha, bias, act, res, y, ws, wsb, NULL)
+
+    assert call(K=1000) == EALIGN
+    assert call(N=1000) == EALIGN
+    assert call(K=133152) == ERANGE
+    assert call(N=0) == ERANGE
+    assert call(T=-1) == EINVAL
+    assert call(alpha=float("nan")) == EINVAL
+    assert call(act=3) == EINVAL
+    assert call(act=-1) == EINVAL
+    assert call(x=NULL) == EINVAL
+    assert call(y=NULL) == EINVAL
+    assert call(bias=p(4098)) == EALIGN
+    assert call(res=p(4104)) == EALIGN
+    assert call(wsb=size - 1) == EWORKSPACE
+    assert call(ws=NULL) == EWORKSPACE
+    assert call(ws=p(4096 + 16)) == EALIGN
+    # the Wq-only variant needs its own, larger workspace
+    assert call(w16=NULL, wsb=min(size, size_wq) - 1) == EWORKSPACE
+    assert call(T=0, x=NULL, y=NULL, bias=p(1), res=p(1), ws=NULL, wsb=0) == OK
