@@ -72,6 +72,7 @@ typedef enum {
 #define I8R_DEV_OK 0
 #define I8R_DEV_PIPELINE_TIMEOUT 1   /* a shared-memory pipeline wait gave up */
 #define I8R_DEV_TMEM_TIMEOUT 2       /* a tensor-memory hand-off wait gave up */
+#define I8R_DEV_BAD_INDEX 3          /* a length, row range or block number on the device is out of range */
 
 /* ---------------------------------------------------------------------------
  * Weight conversion.  The pages describe a 16/32-bit checkpoint converted to
@@ -301,6 +302,56 @@ i8r_status int4_linear(const void *X, int T, int K, const uint8_t *W4, const voi
  * sums up to the order of fp32 additions; the switch (process-wide) exists so
  * that tests and measurements can compare them. */
 void int4_debug_set_product_path(int mode);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit key/value cache.  The FlexGen summary page (research.elamur.ai,
+ * "sheng-2023-flexgen") compresses the KV cache along with the weights; the
+ * codec taken here is this library's 8-bit one, with a scale for each block of
+ * tokens and head:
+ *   - a block is 64 consecutive tokens of one sequence (token t is in the
+ *     sequence's block t / 64, at offset t % 64); heads have D = 64 or 128
+ *     values, and there are H key/value heads;
+ *   - Kc, Vc [num_blocks, H, 64, D] int8   codes
+ *     sK, sV [num_blocks, H] fp32          absmax of what the block's head holds
+ *   - code = clamp(rhaz(x * fl32(127 / s)), -127, 127), and a code stands for
+ *     code * s / 127; s = 0 gives codes 0;
+ *   - block_table [B, max_blocks] int32: the number in [0, num_blocks) of the
+ *     block that holds block i of sequence b; entries past a sequence's length
+ *     are not read;
+ *   - when rows are added to a partly filled block, its scale becomes
+ *     max(old scale, absmax of the new rows), and if that is larger than the
+ *     old one the codes already there become rhaz(code * fl32(old / new)).  A
+ *     block whose first row is added takes the new rows' scale: what a block
+ *     held for an earlier sequence has no effect.
+ * Rows are expected finite.  A NaN or an infinity among a block's rows makes
+ * its scale NaN or infinite, which shows in all the block's values of that head.
+ *
+ * The int32 arrays are read on the device.  A length, row range or block number
+ * out of range is skipped and reported as I8R_DEV_BAD_INDEX in the device status
+ * word (rows that it belongs to are undefined); nothing out of bounds is
+ * touched.
+ *
+ * int8_kv_append: adds rows cu_new[b] .. cu_new[b+1]-1 of K and V to sequence b,
+ *   which holds past[b] tokens, for each of B sequences.  K and V are fp16
+ *   [n_new, H, D]: head h of row r starts at element r*ld + h*D (ldk, ldv >=
+ *   H*D, multiples of 8), so they may be slices of a projection's output.
+ *   past and cu_new are not changed.  The blocks that one call writes must be
+ *   different ones for different sequences (the call does not check this), and
+ *   calls that write the same block must not overlap on the GPU.  n_new = 0 or
+ *   B = 0 is a no-op.
+ * int8_kv_gather: K, V [rows, H, D] fp16 from the cache: tokens 0 .. len-1 of
+ *   sequence b go to rows cu[b] .. cu[b+1]-1, with len = cu[b+1] - cu[b], each
+ *   value fp16_rn(code * fl32(s / 127)).  Rows behind cu[B] are not touched.
+ *   (For attention over a prompt whose beginning is cached.)
+ * ------------------------------------------------------------------------- */
+i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long ldv, int n_new, int H, int D,
+                          const int32_t *cu_new, const int32_t *past, int B,
+                          int8_t *Kc, int8_t *Vc, float *sK, float *sV, int num_blocks,
+                          const int32_t *block_table, int max_blocks, cudaStream_t stream);
+
+i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks,
+                          int H, int D, const int32_t *block_table, int max_blocks,
+                          const int32_t *cu, int B, int rows, void *K, void *V, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Outlier statistics: the outlier feature dimensions of X and the share of

@@ -14,7 +14,7 @@ __all__ = [
     "lib", "I8RError",
     "int8_quantize_weight_colwise", "int8_mixed_linear_workspace_size", "int8_mixed_linear",
     "int8_mixed_linear_wq_workspace_size", "int8_mixed_linear_wq_max_outliers", "int8_mixed_linear_wq",
-    "int8_mixed_linear_fused",
+    "int8_mixed_linear_fused", "KV_BLOCK", "int8_kv_append", "int8_kv_gather",
     "int8_outlier_stats_workspace_size", "int8_outlier_stats", "int8_quantize_activation",
     "int8_gemm_i8_s32", "int8_read_and_clear_device_status", "int8_status_string",
     "int8_selftest_wait_timeout",
@@ -26,11 +26,13 @@ __all__ = [
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libint8row.so")
 DECODE_MAX_T = 128
 INT4_MAX_T = 64
+KV_BLOCK = 64                                          # tokens per block of the 8-bit cache
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2}        # i8r_activation
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 _Z = ctypes.c_size_t
 
 _lib = None
@@ -80,6 +82,8 @@ def lib():
     so.int8_gemm_i8_s32_workspace_size.argtypes = [_I, _I, _I]
     so.int8_gemm_i8_s32_workspace_size.restype = _Z
     so.int8_gemm_i8_s32.argtypes = [_P, _I, _I, _P, _I, _P, _P, _Z, _P]
+    so.int8_kv_append.argtypes = [_P, _L, _P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _P]
+    so.int8_kv_gather.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P]
     so.int8_read_and_clear_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), _P]
     so.int8_selftest_wait_timeout.argtypes = [_I, _P]
     so.int8_selftest_wait_timeout.restype = _I
@@ -100,7 +104,8 @@ def lib():
     so.int4_linear.argtypes = [_P, _I, _I, _P, _P, _I, _P, _P, _Z, _P]
     for name in ("int8_quantize_weight_colwise", "int8_mixed_linear", "int8_mixed_linear_fused", "int8_outlier_stats",
                  "int8_quantize_activation", "int8_gemm_i8_s32", "int8_read_and_clear_device_status",
-                 "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear"):
+                 "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear", "int8_kv_append",
+                 "int8_kv_gather"):
         getattr(so, name).restype = _I
     _lib = so
     return so
@@ -447,3 +452,76 @@ def int4_linear(X, W4, S4, N, Y=None, workspace_buf=None, stream=None):
         _dev(Y, torch.float16, "Y"), ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(),
         _stream(stream)))
     return Y
+
+
+# ---------------------------------------------------------------- the 8-bit key/value cache
+
+def _heads(t, name):
+    """fp16 [rows, heads, D] whose rows may be strided (heads and values contiguous):
+    its pointer and the elements from one row to the next."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions")
+    n, H, D = t.shape
+    if t.numel() == 0 or n == 1 and t.is_contiguous():
+        return ctypes.c_void_p(t.data_ptr()), H * D
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: heads and their values must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else H * D
+
+
+def _cache_args(Kc, Vc, sK, sV, block_table):
+    """The C arguments of a cache, checked: (Kc, Vc, sK, sV, num_blocks), (H, D), (table, max_blocks)."""
+    import torch
+    kc = _dev(Kc, torch.int8, "Kc", 4)
+    blocks, H, tokens, D = Kc.shape
+    _shape(Kc, (blocks, H, KV_BLOCK, D), "Kc")
+    _shape(Vc, Kc.shape, "Vc")
+    _shape(sK, (blocks, H), "sK")
+    _shape(sV, (blocks, H), "sV")
+    table = _dev(block_table, torch.int32, "block_table", 2)
+    return ((kc, _dev(Vc, torch.int8, "Vc"), _dev(sK, torch.float32, "sK"), _dev(sV, torch.float32, "sV"), blocks),
+            (H, D), (table, block_table.shape[1]))
+
+
+def int8_kv_append(K, V, cu_new, past, block_table, Kc, Vc, sK, sV, stream=None):
+    """Add rows cu_new[b]..cu_new[b+1]-1 of K, V (fp16 [n,H,D], rows may be strided) to sequence b
+    of the cache (Kc, Vc int8 [blocks,H,64,D], sK, sV fp32 [blocks,H]), which holds past[b]
+    tokens.  cu_new int32 [B+1], past int32 [B], block_table int32 [B,max_blocks]."""
+    import torch
+    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
+    (k, ldk), (v, ldv) = _heads(K, "K"), _heads(V, "V")
+    _shape(K, (K.shape[0], H, D), "K")
+    _shape(V, K.shape, "V")
+    B = block_table.shape[0]
+    _shape(cu_new, (B + 1,), "cu_new")
+    _shape(past, (B,), "past")
+    with _on(_same_device(K, V, cu_new, past, block_table, Kc, Vc, sK, sV), stream):
+        _check("int8_kv_append", lib().int8_kv_append(
+            k, ldk, v, ldv, K.shape[0], H, D, _dev(cu_new, torch.int32, "cu_new"), _dev(past, torch.int32, "past"), B,
+            *cache, *table, _stream(stream)))
+
+
+def int8_kv_gather(Kc, Vc, sK, sV, cu, block_table, rows, K=None, V=None, stream=None):
+    """-> (K, V) fp16 [rows,H,D]: tokens 0.. of sequence b of the cache in rows cu[b]..cu[b+1]-1
+    (cu int32 [B+1]; rows behind cu[B] are not written)."""
+    import torch
+    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
+    B = block_table.shape[0]
+    _shape(cu, (B + 1,), "cu")
+    shape = (int(rows), H, D)
+    for t, name in ((K, "K"), (V, "V")):
+        if t is not None:
+            _shape(t, shape, name)
+    dev = _same_device(Kc, Vc, sK, sV, cu, block_table, K, V)
+    with _on(dev, stream):
+        K = torch.empty(shape, dtype=torch.float16, device=dev) if K is None else K
+        V = torch.empty(shape, dtype=torch.float16, device=dev) if V is None else V
+        _check("int8_kv_gather", lib().int8_kv_gather(
+            *cache, H, D, *table, _dev(cu, torch.int32, "cu"), B, shape[0], _dev(K, torch.float16, "K"),
+            _dev(V, torch.float16, "V"), _stream(stream)))
+    return K, V

@@ -35,12 +35,14 @@
 #include "gemm_prefill_pair.cuh"
 #include "gemm_decode.cuh"
 #include "gemm_int4.cuh"
+#include "kv_cache.cuh"
 
 namespace {
 
 using namespace i8r;
 
 constexpr int kMaxK = 133144;          // K * 127^2 < 2^31
+constexpr int kMaxHeads = 8192;        // attention and cache heads
 constexpr int kMaxDevices = 64;
 constexpr size_t kAlign = 256;
 
@@ -247,6 +249,11 @@ i8r_status check_ptr(const void *p) {
     return I8R_OK;
 }
 
+
+i8r_status check_index_ptr(const int32_t *p) {
+    if (!p) return I8R_EINVAL;
+    return (reinterpret_cast<uintptr_t>(p) & 3u) ? I8R_EALIGN : I8R_OK;
+}
 
 // Workspace of int8_mixed_linear.
 struct Workspace {
@@ -687,6 +694,46 @@ Int4Workspace int4_ws_layout(int T, int N) {
     return w;
 }
 
+// Heads of the 8-bit cache and of attention: D = 64 or 128.
+i8r_status check_heads(int H, int D) {
+    if (H < 0 || D < 0) return I8R_EINVAL;
+    if (H < 1 || H > kMaxHeads || (D != 64 && D != 128)) return I8R_ERANGE;
+    return I8R_OK;
+}
+
+// A row stride in elements: whole heads fit, 16-byte rows.
+i8r_status check_ld(long long ld, int H, int D) {
+    if (ld < static_cast<long long>(H) * D) return I8R_EINVAL;
+    return ld % 8 ? I8R_EALIGN : I8R_OK;
+}
+
+// The cache's own arguments (int32 arrays need 4-byte alignment only).
+i8r_status check_cache(const void *Kc, const void *Vc, const void *sK, const void *sV, int num_blocks,
+                       const int32_t *block_table, int max_blocks) {
+    if (num_blocks < 0 || max_blocks < 0) return I8R_EINVAL;
+    if (num_blocks == 0 || max_blocks == 0) return I8R_ERANGE;
+    I8R_TRY(check_ptr(Kc));
+    I8R_TRY(check_ptr(Vc));
+    I8R_TRY(check_ptr(sK));
+    I8R_TRY(check_ptr(sV));
+    return check_index_ptr(block_table);
+}
+
+kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks, int H, int D,
+                     const int32_t *block_table, int max_blocks) {
+    kv::Cache c{};
+    c.codes[0] = const_cast<int8_t *>(Kc);
+    c.codes[1] = const_cast<int8_t *>(Vc);
+    c.scale[0] = const_cast<float *>(sK);
+    c.scale[1] = const_cast<float *>(sV);
+    c.num_blocks = num_blocks;
+    c.H = H;
+    c.D = D;
+    c.table = block_table;
+    c.max_blocks = max_blocks;
+    return c;
+}
+
 __global__ void wait_timeout_selftest_kernel(uint64_t limit_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -1112,6 +1159,79 @@ i8r_status int4_linear(const void *X, int T, int K, const uint8_t *W4, const voi
     }
     I8R_LAUNCHED();
     record_after(stream);
+    return I8R_OK;
+}
+
+i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long ldv, int n_new, int H, int D,
+                          const int32_t *cu_new, const int32_t *past, int B, int8_t *Kc, int8_t *Vc, float *sK,
+                          float *sV, int num_blocks, const int32_t *block_table, int max_blocks, cudaStream_t stream) {
+    I8R_TRY(check_heads(H, D));
+    if (n_new < 0 || B < 0) return I8R_EINVAL;
+    I8R_TRY(check_ld(ldk, H, D));
+    I8R_TRY(check_ld(ldv, H, D));
+    if (n_new == 0 || B == 0) return I8R_OK;
+    I8R_TRY(check_ptr(K));
+    I8R_TRY(check_ptr(V));
+    I8R_TRY(check_index_ptr(cu_new));
+    I8R_TRY(check_index_ptr(past));
+    I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
+    const DeviceInfo *dev = nullptr;
+    I8R_TRY(device_setup(&dev));
+    kv::AppendParams p{};
+    p.c = make_cache(Kc, Vc, sK, sV, num_blocks, H, D, block_table, max_blocks);
+    p.x[0] = static_cast<const __half *>(K);
+    p.x[1] = static_cast<const __half *>(V);
+    p.ld[0] = ldk;
+    p.ld[1] = ldv;
+    p.n_new = n_new;
+    p.B = B;
+    p.cu_new = cu_new;
+    p.past = past;
+    // n rows that start anywhere in a block touch at most (n + 126) / 64 blocks, and at most n
+    const long long items = std::min<long long>(n_new, (n_new + 126ll * B) / kv::BLOCK);
+    const dim3 grid(static_cast<unsigned>(items), (2 * H + kv::WARPS - 1) / kv::WARPS);
+    const dim3 block(32 * kv::WARPS);
+    // A warp that keeps a whole block in registers suits prompts (one read of
+    // the rows); for a few rows per sequence the small form's occupancy does.
+    const bool few = n_new <= 8ll * B;
+    if (D == 128 && few)
+        kv::kv_append_kernel<128, 2><<<grid, block, 0, stream>>>(p);
+    else if (D == 128)
+        kv::kv_append_kernel<128, 32><<<grid, block, 0, stream>>>(p);
+    else if (few)
+        kv::kv_append_kernel<64, 2><<<grid, block, 0, stream>>>(p);
+    else
+        kv::kv_append_kernel<64, 16><<<grid, block, 0, stream>>>(p);
+    I8R_LAUNCHED();
+    return I8R_OK;
+}
+
+i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks, int H,
+                          int D, const int32_t *block_table, int max_blocks, const int32_t *cu, int B, int rows, void *K,
+                          void *V, cudaStream_t stream) {
+    I8R_TRY(check_heads(H, D));
+    if (rows < 0 || B < 0) return I8R_EINVAL;
+    if (rows == 0 || B == 0) return I8R_OK;
+    I8R_TRY(check_ptr(K));
+    I8R_TRY(check_ptr(V));
+    I8R_TRY(check_index_ptr(cu));
+    I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
+    const DeviceInfo *dev = nullptr;
+    I8R_TRY(device_setup(&dev));
+    kv::GatherParams p{};
+    p.c = make_cache(Kc, Vc, sK, sV, num_blocks, H, D, block_table, max_blocks);
+    p.out[0] = static_cast<__half *>(K);
+    p.out[1] = static_cast<__half *>(V);
+    p.rows = rows;
+    p.B = B;
+    p.cu = cu;
+    const long long items = std::min<long long>(rows, (rows + 63ll * B) / kv::BLOCK);
+    const dim3 grid(static_cast<unsigned>(items), (2 * H + kv::WARPS - 1) / kv::WARPS);
+    if (D == 128)
+        kv::kv_gather_kernel<128><<<grid, 32 * kv::WARPS, 0, stream>>>(p);
+    else
+        kv::kv_gather_kernel<64><<<grid, 32 * kv::WARPS, 0, stream>>>(p);
+    I8R_LAUNCHED();
     return I8R_OK;
 }
 

@@ -1,0 +1,274 @@
+// The 8-bit key/value cache: appending new rows, and reading rows back.
+//
+// A block is 64 tokens of one sequence.  Per block and key/value head it holds
+// 64 x D int8 codes (contiguous, 8 KB at D = 128) and one fp32 absmax scale, the
+// library's codec: code = clamp(rhaz(x * fl32(127/scale)), +-127), and a code
+// stands for code * scale / 127.  A partly filled block's scale grows with the
+// rows it is given: when the new rows' absmax exceeds the old scale, the codes
+// already there are rescaled once, code' = rhaz(code * fl32(old/new)).
+//
+// Both kernels are bound by HBM: append reads 2 bytes and writes 1 per value,
+// read-back reads 1 and writes 2.  One warp handles one (block, head, K or V):
+// its rows are 16-byte loads with no other warp to wait for.
+#pragma once
+
+#include "device_common.cuh"
+
+namespace i8r {
+namespace kv {
+
+constexpr int BLOCK = 64;            // tokens per cache block
+constexpr int WARPS = 8;             // warps per CTA: one (head, K or V) each
+
+struct Cache {
+    int8_t *codes[2];                // K, V: [num_blocks, H, BLOCK, D]
+    float *scale[2];                 // K, V: [num_blocks, H]
+    int num_blocks, H, D;
+    const int32_t *table;            // [B, max_blocks]
+    int max_blocks;
+};
+
+// The block number that holds block `i` of sequence b, or -1 (reported) when
+// the table has no such entry or it names no block.
+__device__ __forceinline__ int block_of(const int32_t *table, int max_blocks, int num_blocks, int b, int i) {
+    int page = -1;
+    if (i >= 0 && i < max_blocks) page = table[static_cast<size_t>(b) * max_blocks + i];
+    if (page < 0 || page >= num_blocks) {
+        report_status(I8R_DEV_BAD_INDEX);
+        return -1;
+    }
+    return page;
+}
+
+// Which sequence item `item` belongs to, and its place there, when sequence b
+// has count(b) items: a warp adds 128 sequences' counts at a time, four
+// consecutive ones a lane (their loads are in flight together).  Returns -1
+// past the last item.  All lanes get the same answer.
+template <typename Count>
+__device__ __forceinline__ int find_item(long long item, int B, int *place, Count &&count) {
+    const int lane = threadIdx.x & 31;
+    long long base = 0;
+    for (int b0 = 0; b0 < B; b0 += 128) {
+        int n[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = b0 + 4 * lane + j < B ? count(b0 + 4 * lane + j) : 0;
+        const long long mine = static_cast<long long>(n[0]) + n[1] + n[2] + n[3];
+        long long sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, base + sum > item);
+        if (past) {
+            long long left = item - base - (sum - mine);
+            int j = 0;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (j == k && left >= n[k]) left -= n[k], j = k + 1;
+            const int at = __ffs(past) - 1;
+            *place = static_cast<int>(__shfl_sync(0xFFFFFFFFu, left, at));
+            return __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + j, at);
+        }
+        base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    return -1;
+}
+
+// A sequence's row range [lo, hi) in packed rows, from cumulative counts; an
+// inconsistent pair (reported) counts as empty.
+__device__ __forceinline__ int2 row_range(const int32_t *cu, int b, int rows) {
+    const int lo = cu[b], hi = cu[b + 1];
+    if (lo < 0 || hi < lo || hi > rows) {
+        report_status(I8R_DEV_BAD_INDEX);
+        return make_int2(0, 0);
+    }
+    return make_int2(lo, hi);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// Largest magnitude bits of eight fp16 values (a NaN's exceed infinity's, so a
+// NaN makes the scale NaN and shows in every value of its block).
+__device__ __forceinline__ uint32_t max_bits(const uint4 &v, uint32_t m) {
+    m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4 &v, float inv) {
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+        const uint32_t a = static_cast<uint32_t>(quant_code(f.x, inv)) & 0xFFu;
+        const uint32_t b = static_cast<uint32_t>(quant_code(f.y, inv)) & 0xFFu;
+        out[e >> 1] |= (a | (b << 8)) << (16 * (e & 1));
+    }
+    return make_uint2(out[0], out[1]);
+}
+
+struct AppendParams {
+    Cache c;
+    const __half *x[2];              // K, V: new rows, head h of row r at x + r*ld + h*D
+    long long ld[2];
+    int n_new, B;
+    const int32_t *cu_new;           // [B+1]
+    const int32_t *past;             // [B]
+};
+
+// Blocks that sequence b's new rows touch.
+__device__ __forceinline__ int touched_blocks(const AppendParams &p, int b) {
+    const int2 r = row_range(p.cu_new, b, p.n_new);
+    const int past = p.past[b];
+    if (r.x == r.y) return 0;
+    if (past < 0 || past > 0x7FFFFFFF - 2 * BLOCK - (r.y - r.x)) {
+        report_status(I8R_DEV_BAD_INDEX);
+        return 0;
+    }
+    return (past % BLOCK + (r.y - r.x) + BLOCK - 1) / BLOCK;
+}
+
+// One warp per (touched block, head, K or V).  kHold warp-wide loads (a load
+// covers 256/D rows) stay in registers between the absmax and the codes; rows
+// past them are read a second time.  kHold = 64*D/256 holds a whole block (128
+// registers at D = 128) for prompts; single tokens take a small one, so that
+// more warps fit an SM.
+template <int D, int kHold>
+__global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int LANES = D / 8;                   // lanes per row (16 bytes each)
+    constexpr int RPL = 32 / LANES;                // rows per warp-wide load
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / LANES, col = (lane % LANES) * 8;
+    const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
+    if (job >= 2 * p.c.H) return;
+    const int kv = job & 1, head = job >> 1;
+    int place = 0;
+    const int b = find_item(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
+    if (b < 0) return;
+    const int2 range = row_range(p.cu_new, b, p.n_new);
+    const int past = p.past[b];
+    const int i = past / BLOCK + place;                         // the sequence's block
+    const int page = block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, b, i);
+    if (page < 0) return;
+    // tokens [t0, t1) of the sequence are new and in this block
+    const int t0 = max(past, i * BLOCK), t1 = min(past + (range.y - range.x), (i + 1) * BLOCK);
+    const int o0 = t0 - i * BLOCK, n = t1 - t0;                 // offset of the first new row; rows
+    const __half *src = p.x[kv] + static_cast<size_t>(range.x + (t0 - past)) * p.ld[kv] + head * D + col;
+    const size_t at = static_cast<size_t>(page) * p.c.H + head;
+    int8_t *dst = p.c.codes[kv] + at * BLOCK * D;
+    const float old = o0 > 0 ? p.c.scale[kv][at] : 0.0f;
+
+    uint4 v[kHold];
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+        const int r = k * RPL + sub;
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < n) v[k] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv]));
+    }
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) m = max_bits(v[k], m);
+    for (int r = kHold * RPL + sub; r < n; r += RPL)
+        m = max_bits(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), m);
+    m = warp_max(max(m & 0xFFFFu, m >> 16));
+    // non-negative floats order like their bits, and a NaN stays on top
+    const uint32_t top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    const bool grown = top > __float_as_uint(old);
+    const float scale = grown ? __uint_as_float(top) : old;
+    if (lane == 0) p.c.scale[kv][at] = scale;
+    if (grown && old > 0.0f) {
+        // the codes already there, four rows of D = 128 (eight of 64) a load
+        const float ratio = __fdiv_rn(old, scale);
+        for (int e = lane * 16; e < o0 * D; e += 512) {
+            uint4 q = *reinterpret_cast<const uint4 *>(dst + e);
+            uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t out = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float c = static_cast<float>(static_cast<int8_t>((w[j] >> (8 * k)) & 0xFFu));
+                    out |= (static_cast<uint32_t>(quant_code(c, ratio)) & 0xFFu) << (8 * k);
+                }
+                w[j] = out;
+            }
+            *reinterpret_cast<uint4 *>(dst + e) = q;
+        }
+    }
+    const float inv = recip127(scale);
+    dst += static_cast<size_t>(o0) * D + col;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+        const int r = k * RPL + sub;
+        if (r < n) *reinterpret_cast<uint2 *>(dst + r * D) = codes8(v[k], inv);
+    }
+    for (int r = kHold * RPL + sub; r < n; r += RPL)
+        *reinterpret_cast<uint2 *>(dst + r * D) =
+            codes8(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), inv);
+}
+
+struct GatherParams {
+    Cache c;
+    __half *out[2];                  // K, V: [rows, H, D]
+    int rows, B;
+    const int32_t *cu;               // [B+1]: sequence b's tokens are rows cu[b] .. cu[b+1]
+};
+
+// One warp per (block, head, K or V): fp16_rn(code * fl32(scale/127)).
+template <int D>
+__global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const __grid_constant__ GatherParams p) {
+    constexpr int LANES = D / 8;
+    constexpr int RPL = 32 / LANES;
+    constexpr int kAhead = 8;                      // loads in flight per lane
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / LANES, col = (lane % LANES) * 8;
+    const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
+    if (job >= 2 * p.c.H) return;
+    const int kv = job & 1, head = job >> 1;
+    int i = 0;
+    const int b = find_item(blockIdx.x, p.B, &i, [&](int s) {
+        const int2 r = row_range(p.cu, s, p.rows);
+        return (r.y - r.x + BLOCK - 1) / BLOCK;
+    });
+    if (b < 0) return;
+    const int2 range = row_range(p.cu, b, p.rows);
+    const int page = block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, b, i);
+    if (page < 0) return;
+    const int n = min(BLOCK, range.y - range.x - i * BLOCK);
+    const size_t at = static_cast<size_t>(page) * p.c.H + head;
+    const int8_t *src = p.c.codes[kv] + at * BLOCK * D + col;
+    __half *dst = p.out[kv] + (static_cast<size_t>(range.x + i * BLOCK) * p.c.H + head) * D + col;
+    const float step = __fdiv_rn(p.c.scale[kv][at], 127.0f);
+    for (int r0 = 0; r0 < n; r0 += kAhead * RPL) {
+        uint2 q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + k * RPL + sub;
+            q[k] = make_uint2(0u, 0u);
+            if (r < n) q[k] = *reinterpret_cast<const uint2 *>(src + r * D);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + k * RPL + sub;
+            __half2 h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = (e < 2 ? q[k].x : q[k].y) >> (16 * (e & 1));
+                h[e] = __floats2half2_rn(__fmul_rn(static_cast<float>(static_cast<int8_t>(w & 0xFFu)), step),
+                                         __fmul_rn(static_cast<float>(static_cast<int8_t>((w >> 8) & 0xFFu)), step));
+            }
+            if (r < n)
+                *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(r) * p.c.H * D) = *reinterpret_cast<uint4 *>(h);
+        }
+    }
+}
+
+}  // namespace kv
+}  // namespace i8r

@@ -47,3 +47,38 @@ def test_fused_linear_refusals(so):
     # the Wq-only variant needs its own, larger workspace
     assert call(w16=NULL, wsb=min(size, size_wq) - 1) == EWORKSPACE
     assert call(T=0, x=NULL, y=NULL, bias=p(1), res=p(1), ws=NULL, wsb=0) == OK
+
+
+def test_cache_refusals(so):
+    def append(k=p(), ldk=256, ldv=256, n=4, H=2, D=128, cu=p(), past=p(), B=2, kc=p(), sk=p(), blocks=9, table=p(),
+               wide=3):
+        return so.int8_kv_append(k, ldk, p(), ldv, n, H, D, cu, past, B, kc, p(), sk, p(), blocks, table, wide, NULL)
+
+    def gather(kc=p(), sk=p(), blocks=9, H=2, D=128, table=p(), wide=3, cu=p(), B=2, rows=4, k=p()):
+        return so.int8_kv_gather(kc, p(), sk, p(), blocks, H, D, table, wide, cu, B, rows, k, p(), NULL)
+
+    for f in (append, gather):
+        assert f(D=96) == ERANGE
+        assert f(H=0) == ERANGE
+        assert f(H=8193, **(dict(ldk=1 << 21, ldv=1 << 21) if f is append else {})) == ERANGE
+        assert f(H=-1) == EINVAL
+        assert f(B=-1) == EINVAL
+        assert f(blocks=-1) == EINVAL
+        assert f(blocks=0) == ERANGE
+        assert f(wide=0) == ERANGE
+        assert f(kc=NULL) == EINVAL
+        assert f(kc=p(4104)) == EALIGN
+        assert f(sk=NULL) == EINVAL
+        assert f(table=NULL) == EINVAL
+        assert f(table=p(4098)) == EALIGN
+        assert f(cu=NULL) == EINVAL
+        assert f(k=NULL) == EINVAL
+        assert f(k=p(4098)) == EALIGN
+        assert f(B=0, k=NULL) == OK
+    assert append(n=-1) == EINVAL
+    assert append(n=0, k=NULL) == OK
+    assert append(ldk=255) == EINVAL
+    assert append(ldv=260) == EALIGN
+    assert append(past=NULL) == EINVAL
+    assert gather(rows=-1) == EINVAL
+    assert gather(rows=0, k=NULL) == OK
