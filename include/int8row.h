@@ -354,6 +354,38 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
                           const int32_t *cu, int B, int rows, void *K, void *V, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * int8_attention_decode: attention of one query token per sequence over the
+ * 8-bit cache (the step between the QKV and the output projection when tokens
+ * are generated):
+ *   O[b,q,:] = sum_t softmax_t( scale * Q[b,q,:] . K[t,:] ) V[t,:],  t < lengths[b]
+ * with K and V the values the cache's codes stand for, key/value head
+ * h = q / (Hq / H), fp32 scores and sums, and the softmax's weights rounded to
+ * fp16 for the product with V.
+ *
+ *   Q, O     [B, Hq, D] fp16: head q of sequence b starts at element b*ld + q*D
+ *            (ldq, ldo >= Hq*D, multiples of 8); O must not overlap the inputs
+ *   Hq       query heads, a multiple of the H key/value heads
+ *   lengths  [B] int32: tokens of each sequence in the cache, the new one
+ *            included; 0 gives a row of zeros
+ *   scale    finite; usually 1 / sqrt(D)
+ *   workspace  int8_attention_decode_workspace_size(Hq, H, D) bytes, 256-byte
+ *            aligned; its contents on entry are ignored.  Two calls that share a
+ *            workspace must not overlap on the GPU.
+ * Lengths and block numbers are read on the device (a captured call may be
+ * replayed with others); one out of range is reported as I8R_DEV_BAD_INDEX and
+ * leaves the rows of its sequence undefined.  The cache is only read: a block may
+ * stand in several sequences' tables.  The result does not depend on timing: the
+ * same inputs on the same GPU give the same bits.
+ * ------------------------------------------------------------------------- */
+size_t int8_attention_decode_workspace_size(int Hq, int H, int D);
+
+i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, int H, int D,
+                                 const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks,
+                                 const int32_t *block_table, int max_blocks, const int32_t *lengths,
+                                 float scale, void *O, long long ldo,
+                                 void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Outlier statistics: the outlier feature dimensions of X and the share of
  * values that go through the 8-bit product (the pages report that share as
  * above 99.9% on large models; LLM.int8() abstract).

@@ -15,6 +15,7 @@ __all__ = [
     "int8_quantize_weight_colwise", "int8_mixed_linear_workspace_size", "int8_mixed_linear",
     "int8_mixed_linear_wq_workspace_size", "int8_mixed_linear_wq_max_outliers", "int8_mixed_linear_wq",
     "int8_mixed_linear_fused", "KV_BLOCK", "int8_kv_append", "int8_kv_gather",
+    "int8_attention_decode_workspace_size", "int8_attention_decode",
     "int8_outlier_stats_workspace_size", "int8_outlier_stats", "int8_quantize_activation",
     "int8_gemm_i8_s32", "int8_read_and_clear_device_status", "int8_status_string",
     "int8_selftest_wait_timeout",
@@ -84,6 +85,9 @@ def lib():
     so.int8_gemm_i8_s32.argtypes = [_P, _I, _I, _P, _I, _P, _P, _Z, _P]
     so.int8_kv_append.argtypes = [_P, _L, _P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _P]
     so.int8_kv_gather.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _P]
+    so.int8_attention_decode_workspace_size.argtypes = [_I, _I, _I]
+    so.int8_attention_decode_workspace_size.restype = _Z
+    so.int8_attention_decode.argtypes = [_P, _L, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _F, _P, _L, _P, _Z, _P]
     so.int8_read_and_clear_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), _P]
     so.int8_selftest_wait_timeout.argtypes = [_I, _P]
     so.int8_selftest_wait_timeout.restype = _I
@@ -105,7 +109,7 @@ def lib():
     for name in ("int8_quantize_weight_colwise", "int8_mixed_linear", "int8_mixed_linear_fused", "int8_outlier_stats",
                  "int8_quantize_activation", "int8_gemm_i8_s32", "int8_read_and_clear_device_status",
                  "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear", "int8_kv_append",
-                 "int8_kv_gather"):
+                 "int8_kv_gather", "int8_attention_decode"):
         getattr(so, name).restype = _I
     _lib = so
     return so
@@ -525,3 +529,33 @@ def int8_kv_gather(Kc, Vc, sK, sV, cu, block_table, rows, K=None, V=None, stream
             *cache, H, D, *table, _dev(cu, torch.int32, "cu"), B, shape[0], _dev(K, torch.float16, "K"),
             _dev(V, torch.float16, "V"), _stream(stream)))
     return K, V
+
+
+def int8_attention_decode_workspace_size(Hq, H, D):
+    return int(lib().int8_attention_decode_workspace_size(int(Hq), int(H), int(D)))
+
+
+def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O=None, workspace_buf=None, stream=None):
+    """O fp16 [B,Hq,D]: attention of one query token per sequence (Q fp16 [B,Hq,D], rows may be
+    strided) over the first lengths[b] tokens of the 8-bit cache.  scale defaults to 1/sqrt(D)."""
+    import torch
+    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
+    q, ldq = _heads(Q, "Q")
+    B, Hq = Q.shape[0], Q.shape[1]
+    _shape(Q, (block_table.shape[0], Hq, D), "Q")
+    _shape(lengths, (B,), "lengths")
+    if O is not None:
+        _shape(O, Q.shape, "O")
+    dev = _same_device(Q, Kc, Vc, sK, sV, block_table, lengths, O, workspace_buf)
+    with _on(dev, stream):
+        O = torch.empty((B, Hq, D), dtype=torch.float16, device=dev) if O is None else O
+        if workspace_buf is None:
+            workspace_buf = torch.empty(max(1, int8_attention_decode_workspace_size(Hq, H, D)), dtype=torch.uint8,
+                                        device=dev)
+        ws = workspace_buf
+        o, ldo = _heads(O, "O")
+        _check("int8_attention_decode", lib().int8_attention_decode(
+            q, ldq, B, Hq, H, D, *cache, *table, _dev(lengths, torch.int32, "lengths"),
+            1.0 / D ** 0.5 if scale is None else float(scale), o, ldo, ctypes.c_void_p(ws.data_ptr()),
+            ws.numel() * ws.element_size(), _stream(stream)))
+    return O

@@ -36,6 +36,7 @@
 #include "gemm_decode.cuh"
 #include "gemm_int4.cuh"
 #include "kv_cache.cuh"
+#include "attention_decode.cuh"
 
 namespace {
 
@@ -135,6 +136,20 @@ i8r_status set_int4_small_attributes() {
     return I8R_OK;
 }
 
+template <int D, int NT>
+cudaError_t set_decode_attention_attribute() {
+    return cudaFuncSetAttribute(attn::attention_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                NT == 1 ? 112 * 1024 : 226 * 1024);
+}
+
+i8r_status set_attention_attributes() {
+    I8R_CUDA((set_decode_attention_attribute<64, 1>()));
+    I8R_CUDA((set_decode_attention_attribute<64, 2>()));
+    I8R_CUDA((set_decode_attention_attribute<128, 1>()));
+    I8R_CUDA((set_decode_attention_attribute<128, 2>()));
+    return I8R_OK;
+}
+
 i8r_status device_setup(const DeviceInfo **out) {
     int dev = 0;
     I8R_CUDA(cudaGetDevice(&dev));
@@ -178,6 +193,7 @@ i8r_status device_setup(const DeviceInfo **out) {
             I8R_CUDA(cudaFuncSetAttribute(w4::gemm_int4_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(w4::SMEM_BUDGET + 4096)));
             I8R_TRY(set_int4_small_attributes());
+            I8R_TRY(set_attention_attributes());
             I8R_CUDA(cudaFuncSetAttribute(activation_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(kFusedSmemMax)));
             int per_sm = 0;
@@ -719,6 +735,31 @@ i8r_status check_cache(const void *Kc, const void *Vc, const void *sK, const voi
     return check_index_ptr(block_table);
 }
 
+// Query heads: a multiple of the key/value heads.
+i8r_status check_groups(int Hq, int H, int D) {
+    if (Hq < 0) return I8R_EINVAL;
+    I8R_TRY(check_heads(H, D));
+    if (Hq > kMaxHeads || Hq < H || Hq % H) return I8R_ERANGE;
+    return I8R_OK;
+}
+
+// How int8_attention_decode cuts a key/value head's queries: into tiles of at
+// most 16, as even as they come (a tile reads the head's codes once).
+struct DecodeTiles {
+    int G, GT, tile;
+    DecodeTiles(int Hq, int H) : G(Hq / H), GT((G + 15) / 16), tile((G + GT - 1) / GT) {}
+    bool wide() const { return tile > 8; }         // two 8-query MMA columns
+};
+
+// Ring stages of the decode attention's warps: what shared memory leaves, two
+// CTAs an SM for up to 8 queries and one for 16, from 2 to 4.
+int decode_attention_stages(const DecodeTiles &q, int D) {
+    const size_t budget = q.wide() ? 226 * 1024 : 112 * 1024;
+    int stages = 4;
+    while (stages > 2 && attn::decode_smem(q.tile, D, stages) > budget) --stages;
+    return stages;
+}
+
 kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks, int H, int D,
                      const int32_t *block_table, int max_blocks) {
     kv::Cache c{};
@@ -732,6 +773,28 @@ kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const 
     c.table = block_table;
     c.max_blocks = max_blocks;
     return c;
+}
+
+template <int D>
+i8r_status launch_decode_attention(const DeviceInfo *dev, attn::DecodeParams p, const DecodeTiles &q, cudaStream_t s) {
+    p.stages = decode_attention_stages(q, D);
+    const size_t smem = attn::decode_smem(q.tile, D, p.stages);
+    const int ctas = std::min((q.wide() ? 1 : 2) * dev->sms, attn::DEC_MAX_CTAS);
+    if (q.wide())
+        attn::attention_decode_kernel<D, 2><<<ctas, attn::DEC_THREADS, smem, s>>>(p);
+    else
+        attn::attention_decode_kernel<D, 1><<<ctas, attn::DEC_THREADS, smem, s>>>(p);
+    I8R_LAUNCHED();
+    if (ctas > 1) {
+        const cudaError_t e = launch_dependent(attn::attention_combine_kernel<D>, dim3(ctas - 1, q.tile), dim3(D), 0, s, 1,
+                                               p, ctas);
+        if (e != cudaSuccess) {
+            tl_last_cuda_error = static_cast<int>(e);
+            return I8R_ECUDA;
+        }
+        I8R_LAUNCHED();
+    }
+    return I8R_OK;
 }
 
 __global__ void wait_timeout_selftest_kernel(uint64_t limit_ns) {
@@ -1233,6 +1296,46 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
         kv::kv_gather_kernel<64><<<grid, 32 * kv::WARPS, 0, stream>>>(p);
     I8R_LAUNCHED();
     return I8R_OK;
+}
+
+size_t int8_attention_decode_workspace_size(int Hq, int H, int D) {
+    if (check_groups(Hq, H, D) != I8R_OK) return 0;
+    const DecodeTiles q(Hq, H);
+    return align_up(2 * attn::DEC_MAX_CTAS * static_cast<size_t>(attn::piece_floats(q.tile, D)) * 4);
+}
+
+i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, int H, int D, const int8_t *Kc,
+                                 const int8_t *Vc, const float *sK, const float *sV, int num_blocks,
+                                 const int32_t *block_table, int max_blocks, const int32_t *lengths, float scale,
+                                 void *O, long long ldo, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    I8R_TRY(check_groups(Hq, H, D));
+    if (B < 0 || !std::isfinite(scale)) return I8R_EINVAL;
+    I8R_TRY(check_ld(ldq, Hq, D));
+    I8R_TRY(check_ld(ldo, Hq, D));
+    if (B == 0) return I8R_OK;
+    I8R_TRY(check_ptr(Q));
+    I8R_TRY(check_ptr(O));
+    I8R_TRY(check_index_ptr(lengths));
+    I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
+    if (!workspace || workspace_bytes < int8_attention_decode_workspace_size(Hq, H, D)) return I8R_EWORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return I8R_EALIGN;
+    const DeviceInfo *dev = nullptr;
+    I8R_TRY(device_setup(&dev));
+    const DecodeTiles q(Hq, H);
+    attn::DecodeParams p{};
+    p.c = make_cache(Kc, Vc, sK, sV, num_blocks, H, D, block_table, max_blocks);
+    p.Q = static_cast<const __half *>(Q);
+    p.O = static_cast<__half *>(O);
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.lengths = lengths;
+    p.B = B;
+    p.G = q.G;
+    p.GT = q.GT;
+    p.tile = q.tile;
+    p.scale_log2 = scale * 1.44269504088896340736f;      // log2(e)
+    p.part = static_cast<float *>(workspace);
+    return D == 128 ? launch_decode_attention<128>(dev, p, q, stream) : launch_decode_attention<64>(dev, p, q, stream);
 }
 
 i8r_status int8_read_and_clear_device_status(int *code, cudaStream_t stream) {

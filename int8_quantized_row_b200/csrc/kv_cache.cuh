@@ -45,14 +45,14 @@ __device__ __forceinline__ int block_of(const int32_t *table, int max_blocks, in
 // consecutive ones a lane (their loads are in flight together).  Returns -1
 // past the last item.  All lanes get the same answer.
 template <typename Count>
-__device__ __forceinline__ int find_item(long long item, int B, int *place, Count &&count) {
+__device__ __forceinline__ int find_item(long long item, int B, long long *place, Count &&count) {
     const int lane = threadIdx.x & 31;
     long long base = 0;
     for (int b0 = 0; b0 < B; b0 += 128) {
-        int n[4];
+        long long n[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) n[j] = b0 + 4 * lane + j < B ? count(b0 + 4 * lane + j) : 0;
-        const long long mine = static_cast<long long>(n[0]) + n[1] + n[2] + n[3];
+        const long long mine = n[0] + n[1] + n[2] + n[3];
         long long sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ int find_item(long long item, int B, int *place, Coun
             for (int k = 0; k < 3; ++k)
                 if (j == k && left >= n[k]) left -= n[k], j = k + 1;
             const int at = __ffs(past) - 1;
-            *place = static_cast<int>(__shfl_sync(0xFFFFFFFFu, left, at));
+            *place = __shfl_sync(0xFFFFFFFFu, left, at);
             return __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + j, at);
         }
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const __grid_cons
     const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
     if (job >= 2 * p.c.H) return;
     const int kv = job & 1, head = job >> 1;
-    int place = 0;
+    long long place = 0;
     const int b = find_item(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
     if (b < 0) return;
     const int2 range = row_range(p.cu_new, b, p.n_new);
     const int past = p.past[b];
-    const int i = past / BLOCK + place;                         // the sequence's block
+    const int i = past / BLOCK + static_cast<int>(place);                    // the sequence's block
     const int page = block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, b, i);
     if (page < 0) return;
     // tokens [t0, t1) of the sequence are new and in this block
@@ -232,13 +232,14 @@ __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const __grid_cons
     const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
     if (job >= 2 * p.c.H) return;
     const int kv = job & 1, head = job >> 1;
-    int i = 0;
-    const int b = find_item(blockIdx.x, p.B, &i, [&](int s) {
+    long long place = 0;
+    const int b = find_item(blockIdx.x, p.B, &place, [&](int s) {
         const int2 r = row_range(p.cu, s, p.rows);
         return (r.y - r.x + BLOCK - 1) / BLOCK;
     });
     if (b < 0) return;
     const int2 range = row_range(p.cu, b, p.rows);
+    const int i = static_cast<int>(place);
     const int page = block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, b, i);
     if (page < 0) return;
     const int n = min(BLOCK, range.y - range.x - i * BLOCK);

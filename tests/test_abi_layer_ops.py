@@ -82,3 +82,37 @@ def test_cache_refusals(so):
     assert append(past=NULL) == EINVAL
     assert gather(rows=-1) == EINVAL
     assert gather(rows=0, k=NULL) == OK
+
+
+def test_decode_attention_refusals(so):
+    size = so.int8_attention_decode_workspace_size
+    f = so.int8_attention_decode
+
+    def call(q=p(), ldq=512, B=2, Hq=4, H=2, D=128, kc=p(), blocks=9, table=p(), wide=3, lens=p(), scale=0.1, o=p(),
+             ldo=512, ws=p(), wsb=None):
+        wsb = size(Hq, H, D) if wsb is None else wsb
+        return f(q, ldq, B, Hq, H, D, kc, p(), p(), p(), blocks, table, wide, lens, scale, o, ldo, ws, wsb, NULL)
+
+    assert size(4, 2, 128) > 0 and size(4, 3, 128) == 0 and size(4, 2, 80) == 0 and size(-1, 2, 64) == 0
+    assert call(D=32, wsb=1 << 30) == ERANGE
+    assert call(Hq=5, wsb=1 << 30) == ERANGE
+    assert call(Hq=1, wsb=1 << 30) == ERANGE
+    assert call(Hq=-4, wsb=1 << 30) == EINVAL
+    assert call(H=0, wsb=1 << 30) == ERANGE
+    assert call(B=-1) == EINVAL
+    assert call(scale=float("nan")) == EINVAL
+    assert call(scale=float("inf")) == EINVAL
+    assert call(ldq=511) == EINVAL
+    assert call(ldo=516) == EALIGN
+    assert call(q=NULL) == EINVAL
+    assert call(o=p(4104)) == EALIGN
+    assert call(lens=NULL) == EINVAL
+    assert call(lens=p(4097)) == EALIGN
+    assert call(kc=NULL) == EINVAL
+    assert call(blocks=0) == ERANGE
+    assert call(wide=0) == ERANGE
+    assert call(table=NULL) == EINVAL
+    assert call(wsb=size(4, 2, 128) - 1) == EWORKSPACE
+    assert call(ws=NULL) == EWORKSPACE
+    assert call(ws=p(4096 + 64)) == EALIGN
+    assert call(B=0, q=NULL, ws=NULL, wsb=0) == OK
