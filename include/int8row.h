@@ -386,6 +386,35 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * int8_attention_prompt: causal attention over packed prompts of different
+ * lengths (the step between the QKV and the output projection when prompts are
+ * read), fp16 in and out:
+ *   sequence b has nq = cu_q[b+1] - cu_q[b] query rows, rows cu_q[b] .. of Q,
+ *   and nk = cu_k[b+1] - cu_k[b] key rows, rows cu_k[b] .. of K and V; its query
+ *   row i sees its keys 0 .. i + nk - nq (nk > nq: the first nk - nq keys come
+ *   from before the queries, e.g. out of int8_kv_gather):
+ *   O[i,q,:] = sum_k softmax_k( scale * Q[i,q,:] . K[k,h,:] ) V[k,h,:],  h = q / (Hq / H)
+ * with fp32 scores and sums, and the softmax's weights rounded to fp16 for the
+ * product with V.  A row that sees no key (nk < nq) is zeros.
+ *
+ *   Q, O   [N, Hq, D], K, V [M, H, D] fp16: head q of row i starts at element
+ *          i*ld + q*D (every ld at least its heads times D and a multiple of 8),
+ *          so they may be slices of a projection's output; O must not overlap
+ *          the inputs
+ *   D      64 or 128; Hq a multiple of H
+ *   cu_q, cu_k [B+1] int32, cumulative, on the device
+ *   scale  finite; usually 1 / sqrt(D)
+ * Keys and values that a row does not see have no effect on it, infinities and
+ * NaN included.  Rows of O that belong to no sequence are not touched.  A row
+ * range that is out of order or past N or M is reported as I8R_DEV_BAD_INDEX and
+ * counts as empty.  The call needs no workspace.  N = 0 or B = 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, long long ldk, const void *V,
+                                 long long ldv, int N, int M, int Hq, int H, int D,
+                                 const int32_t *cu_q, const int32_t *cu_k, int B, float scale,
+                                 void *O, long long ldo, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Outlier statistics: the outlier feature dimensions of X and the share of
  * values that go through the 8-bit product (the pages report that share as
  * above 99.9% on large models; LLM.int8() abstract).

@@ -15,7 +15,7 @@ __all__ = [
     "int8_quantize_weight_colwise", "int8_mixed_linear_workspace_size", "int8_mixed_linear",
     "int8_mixed_linear_wq_workspace_size", "int8_mixed_linear_wq_max_outliers", "int8_mixed_linear_wq",
     "int8_mixed_linear_fused", "KV_BLOCK", "int8_kv_append", "int8_kv_gather",
-    "int8_attention_decode_workspace_size", "int8_attention_decode",
+    "int8_attention_decode_workspace_size", "int8_attention_decode", "int8_attention_prompt",
     "int8_outlier_stats_workspace_size", "int8_outlier_stats", "int8_quantize_activation",
     "int8_gemm_i8_s32", "int8_read_and_clear_device_status", "int8_status_string",
     "int8_selftest_wait_timeout",
@@ -88,6 +88,7 @@ def lib():
     so.int8_attention_decode_workspace_size.argtypes = [_I, _I, _I]
     so.int8_attention_decode_workspace_size.restype = _Z
     so.int8_attention_decode.argtypes = [_P, _L, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _F, _P, _L, _P, _Z, _P]
+    so.int8_attention_prompt.argtypes = [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _P, _P, _I, _F, _P, _L, _P]
     so.int8_read_and_clear_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), _P]
     so.int8_selftest_wait_timeout.argtypes = [_I, _P]
     so.int8_selftest_wait_timeout.restype = _I
@@ -109,7 +110,7 @@ def lib():
     for name in ("int8_quantize_weight_colwise", "int8_mixed_linear", "int8_mixed_linear_fused", "int8_outlier_stats",
                  "int8_quantize_activation", "int8_gemm_i8_s32", "int8_read_and_clear_device_status",
                  "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear", "int8_kv_append",
-                 "int8_kv_gather", "int8_attention_decode"):
+                 "int8_kv_gather", "int8_attention_decode", "int8_attention_prompt"):
         getattr(so, name).restype = _I
     _lib = so
     return so
@@ -558,4 +559,30 @@ def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O
             q, ldq, B, Hq, H, D, *cache, *table, _dev(lengths, torch.int32, "lengths"),
             1.0 / D ** 0.5 if scale is None else float(scale), o, ldo, ctypes.c_void_p(ws.data_ptr()),
             ws.numel() * ws.element_size(), _stream(stream)))
+    return O
+
+
+def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=None):
+    """O fp16 [N,Hq,D]: causal attention over packed sequences.  Q fp16 [N,Hq,D], K, V fp16 [M,H,D]
+    (rows may be strided); sequence b has query rows cu_q[b]..cu_q[b+1]-1 and key rows
+    cu_k[b]..cu_k[b+1]-1 (cu_k defaults to cu_q), the last of each aligned.  scale defaults to
+    1/sqrt(D).  Rows of O that belong to no sequence are not written."""
+    import torch
+    cu_k = cu_q if cu_k is None else cu_k
+    (q, ldq), (k, ldk), (v, ldv) = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V")
+    (N, Hq, D), (M, H) = Q.shape, K.shape[:2]
+    _shape(K, (M, H, D), "K")
+    _shape(V, K.shape, "V")
+    B = cu_q.numel() - 1
+    _shape(cu_q, (max(B, 0) + 1,), "cu_q")
+    _shape(cu_k, cu_q.shape, "cu_k")
+    if O is not None:
+        _shape(O, Q.shape, "O")
+    dev = _same_device(Q, K, V, cu_q, cu_k, O)
+    with _on(dev, stream):
+        O = torch.empty((N, Hq, D), dtype=torch.float16, device=dev) if O is None else O
+        o, ldo = _heads(O, "O")
+        _check("int8_attention_prompt", lib().int8_attention_prompt(
+            q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, _dev(cu_q, torch.int32, "cu_q"), _dev(cu_k, torch.int32, "cu_k"), B,
+            1.0 / D ** 0.5 if scale is None else float(scale), o, ldo, _stream(stream)))
     return O

@@ -206,7 +206,7 @@ struct State {
     }
 
     __device__ __forceinline__ void step(const DecodeParams &p, const Place &w, const uint8_t *slot) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const int lane = threadIdx.x & 31, g = lane >> 2;
         const uint8_t *mine = slot + lane * 16;
         const float2 sc = *reinterpret_cast<const float2 *>(slot + 2 * STEP * D);
         float x[NT][4];

@@ -37,6 +37,7 @@
 #include "gemm_int4.cuh"
 #include "kv_cache.cuh"
 #include "attention_decode.cuh"
+#include "attention_prompt.cuh"
 
 namespace {
 
@@ -147,6 +148,10 @@ i8r_status set_attention_attributes() {
     I8R_CUDA((set_decode_attention_attribute<64, 2>()));
     I8R_CUDA((set_decode_attention_attribute<128, 1>()));
     I8R_CUDA((set_decode_attention_attribute<128, 2>()));
+    I8R_CUDA(cudaFuncSetAttribute(attn::attention_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(attn::PromptShape<64>::SMEM)));
+    I8R_CUDA(cudaFuncSetAttribute(attn::attention_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(attn::PromptShape<128>::SMEM)));
     return I8R_OK;
 }
 
@@ -214,12 +219,13 @@ i8r_status device_setup(const DeviceInfo **out) {
 // 128-byte swizzle unless asked otherwise, zero fill out of bounds on loads.
 // `promote` widens the L2 fetch of each box row (256 B helps when the next
 // 128 B are read soon by the same CTA; it doubles DRAM reads when they are not).
+// `ld`: elements from row to row where that is not `cols`.
 i8r_status make_map(CUtensorMap *map, const void *base, CUtensorMapDataType type, int elem, uint64_t rows,
                     uint64_t cols, uint32_t box_rows, uint32_t box_cols,
                     CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, uint64_t ld = 0) {
     const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * static_cast<uint64_t>(elem)};
+    const cuuint64_t strides[1] = {(ld ? ld : cols) * static_cast<uint64_t>(elem)};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
@@ -797,6 +803,13 @@ i8r_status launch_decode_attention(const DeviceInfo *dev, attn::DecodeParams p, 
     return I8R_OK;
 }
 
+// A packed [rows, H, D] fp16 tensor with row stride ld, in boxes of 128 rows and
+// 64 values (one 128-byte swizzle span).
+i8r_status make_heads_map(CUtensorMap *map, const void *base, int rows, int H, int D, long long ld) {
+    return make_map(map, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, static_cast<uint64_t>(H) * D, attn::PT, 64,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_128B, static_cast<uint64_t>(ld));
+}
+
 __global__ void wait_timeout_selftest_kernel(uint64_t limit_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -1336,6 +1349,63 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     p.scale_log2 = scale * 1.44269504088896340736f;      // log2(e)
     p.part = static_cast<float *>(workspace);
     return D == 128 ? launch_decode_attention<128>(dev, p, q, stream) : launch_decode_attention<64>(dev, p, q, stream);
+}
+
+i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, long long ldk, const void *V,
+                                 long long ldv, int N, int M, int Hq, int H, int D, const int32_t *cu_q,
+                                 const int32_t *cu_k, int B, float scale, void *O, long long ldo,
+                                 cudaStream_t stream) {
+    I8R_TRY(check_groups(Hq, H, D));
+    if (N < 0 || M < 0 || B < 0 || !std::isfinite(scale)) return I8R_EINVAL;
+    I8R_TRY(check_ld(ldq, Hq, D));
+    I8R_TRY(check_ld(ldk, H, D));
+    I8R_TRY(check_ld(ldv, H, D));
+    I8R_TRY(check_ld(ldo, Hq, D));
+    if (N == 0 || B == 0) return I8R_OK;
+    I8R_TRY(check_ptr(Q));
+    I8R_TRY(check_ptr(O));
+    if (M > 0) {
+        I8R_TRY(check_ptr(K));
+        I8R_TRY(check_ptr(V));
+    }
+    I8R_TRY(check_index_ptr(cu_q));
+    I8R_TRY(check_index_ptr(cu_k));
+    // tiles of 256 rows: at most one part-filled tile a sequence, and none without a row
+    const long long tiles = std::min<long long>(N, (N + (attn::PROMPT_ROWS - 1ll) * B) / attn::PROMPT_ROWS);
+    if (tiles * Hq > 0x7FFFFFFFll) return I8R_ERANGE;
+    const DeviceInfo *dev = nullptr;
+    I8R_TRY(device_setup(&dev));
+    CUtensorMap map_q, map_k, map_v;
+    I8R_TRY(make_heads_map(&map_q, Q, N, Hq, D, ldq));
+    map_k = map_v = map_q;               // unused without keys
+    if (M > 0) {
+        I8R_TRY(make_heads_map(&map_k, K, M, H, D, ldk));
+        I8R_TRY(make_heads_map(&map_v, V, M, H, D, ldv));
+    }
+    attn::PromptParams p{};
+    p.O = static_cast<__half *>(O);
+    p.ldo = ldo;
+    p.N = N;
+    p.M = M;
+    p.B = B;
+    p.Hq = Hq;
+    p.H = H;
+    p.G = Hq / H;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    // a negative scale negates the scores in the MMA, and 0 becomes a scale that
+    // leaves every finite score at 0 (infinities, the masked places, stay)
+    p.scale_log2 = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
+    p.negate = scale < 0.0f ? 1u << 13 : 0u;
+    const dim3 grid(static_cast<unsigned>(tiles * Hq));
+    if (D == 128)
+        attn::attention_prompt_kernel<128><<<grid, attn::PROMPT_THREADS, attn::PromptShape<128>::SMEM, stream>>>(
+            map_q, map_k, map_v, p);
+    else
+        attn::attention_prompt_kernel<64><<<grid, attn::PROMPT_THREADS, attn::PromptShape<64>::SMEM, stream>>>(
+            map_q, map_k, map_v, p);
+    I8R_LAUNCHED();
+    return I8R_OK;
 }
 
 i8r_status int8_read_and_clear_device_status(int *code, cudaStream_t stream) {

@@ -116,3 +116,31 @@ def test_decode_attention_refusals(so):
     assert call(ws=NULL) == EWORKSPACE
     assert call(ws=p(4096 + 64)) == EALIGN
     assert call(B=0, q=NULL, ws=NULL, wsb=0) == OK
+
+
+def test_prompt_attention_refusals(so):
+    def call(q=p(), ldq=512, k=p(), ldk=256, v=p(), ldv=256, N=9, M=9, Hq=4, H=2, D=128, cq=p(), ck=p(), B=2, scale=0.1,
+             o=p(), ldo=512):
+        return so.int8_attention_prompt(q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, scale, o, ldo, NULL)
+
+    assert call(D=256, ldq=4096, ldk=4096, ldv=4096, ldo=4096) == ERANGE
+    assert call(Hq=3) == ERANGE
+    assert call(Hq=0) == ERANGE
+    assert call(H=-2) == EINVAL
+    assert call(N=-1) == EINVAL
+    assert call(M=-1) == EINVAL
+    assert call(B=-1) == EINVAL
+    assert call(scale=float("nan")) == EINVAL
+    assert call(scale=float("-inf")) == EINVAL
+    for name, least in (("ldq", 512), ("ldk", 256), ("ldv", 256), ("ldo", 512)):
+        assert call(**{name: least - 8}) == EINVAL
+        assert call(**{name: least + 4}) == EALIGN
+    for name in ("q", "k", "v", "o"):
+        assert call(**{name: NULL}) == EINVAL
+        assert call(**{name: p(4104)}) == EALIGN
+    for name in ("cq", "ck"):
+        assert call(**{name: NULL}) == EINVAL
+        assert call(**{name: p(4097)}) == EALIGN
+    assert call(N=1 << 30, B=1, Hq=8192, H=8192, ldq=1 << 20, ldk=1 << 20, ldv=1 << 20, ldo=1 << 20) == ERANGE
+    assert call(N=0, q=NULL) == OK
+    assert call(B=0, q=NULL) == OK
