@@ -6,35 +6,43 @@
 // in one pass over the codes with a running maximum and sum.
 //
 // Bound by reading the codes from HBM once (2 D bytes a token and head), so the
-// work is cut by bytes: a step is 16 tokens of one (sequence, key/value head,
-// tile of 8*NT queries), all steps of the call in order are dealt to the warps of
-// a persistent grid in equal contiguous ranges, and every warp works through its
-// range alone.  A range usually begins and ends inside an item; those pieces are
-// merged per CTA in shared memory, and the few items that cross CTAs by
-// combine_kernel from at most two pieces a CTA, always in the same order.
+// work is cut by bytes: an item is one (sequence, key/value head, tile of up to
+// 8*NT queries), all items' tokens in order are dealt in steps of 16 to the warps
+// of a persistent grid in equal contiguous ranges, and every warp works through
+// its range alone, a block of 64 tokens at a time (fewer at the range's ends).
+// Ranges usually begin and end inside an item; those pieces are merged per CTA in
+// shared memory, and the few items that cross CTAs by attention_combine_kernel
+// from at most two pieces a CTA, always in the same order.
 //
-// The codes travel by cp.async into slots that only the copying lane reads (the
-// ring is the lanes' registers, spilled: no barrier, no bank conflict, and three
-// steps in flight for a 16-warp SM are about 128 KB), laid out so that a lane
-// gets its own mma.sync fragments: m16n8k16 with tokens (then values' columns) as
-// the 16 rows and queries as the 8 columns, which suits one to eight queries per
-// head; at under one MMA per 10 cycles the legacy tensor path is nowhere near a
-// limit.  Codes become fp16 exactly (byte permutes against 0x6400 and one
-// subtraction), scores and sums are fp32, and p = e^(x - max) <= 1 is rounded to
-// fp16 (2^-11) for the second product, below the rounding of the fp16 output.
+// The codes travel by cp.async into slots that only the copying lane reads (they
+// are its registers to come: no barrier, no bank conflict), eight sub-tiles of 16
+// tokens of K or V a warp, each asked for again as soon as it has been read, so a
+// whole block per warp is always on its way.  A lane's bytes are its own mma.sync
+// fragments: m16n8k16 with tokens (then V's columns) as the 16 rows and queries as
+// the 8 columns, which suits one to eight queries per head; at one MMA in ten
+// cycles the legacy tensor path is nowhere near a limit.
+//
+// What counts besides bytes is instructions, most of them to turn codes into fp16:
+// xor 0x80 and a byte permute against 0x64 make 1024 + (code + 128), exactly.  For V
+// a subtraction takes the 1152 off again.  For K they stay in the operand and the
+// scores start at -1152 sum(Q) instead, which costs fp32 sums of that size: an error
+// of about 1152 * 2^-24 = 0.00007 of a code per step, before the scale, where the
+// codec itself rounds to half a code (V's sums, which become the output, are kept
+// exact).  p = e^(x - max) <= 1 is rounded to fp16 (2^-11) for the second product,
+// as the output will be, and the softmax's sum is that of the rounded p (one more
+// MMA, with ones for V).  The sums over V are kept in units of the current block's
+// scale, so the MMAs accumulate in place.
 #pragma once
 
 #include "device_common.cuh"
-#include "gemm_decode.cuh"
 #include "kv_cache.cuh"
 
 namespace i8r {
 namespace attn {
 
-constexpr int STEP = 16;                 // tokens per step
-constexpr int DEC_WARPS = 8;
-constexpr int DEC_THREADS = 32 * DEC_WARPS;
-constexpr int DEC_MAX_CTAS = 320;        // of the persistent grid (two per SM), which sizes the workspace
+constexpr int STEP = 16;                 // tokens per step: the granularity of the ranges
+constexpr int SUBS = kv::BLOCK / STEP;   // steps per block
+constexpr int DEC_MAX_CTAS = 160;        // of the persistent grid (one per SM), which sizes the workspace
 
 struct DecodeParams {
     kv::Cache c;
@@ -43,24 +51,30 @@ struct DecodeParams {
     long long ldq, ldo;
     const int32_t *lengths;
     int B, G, GT, tile;                  // queries per kv head, tiles of `tile` queries per kv head
-    float scale_log2;                    // scale * log2(e)
+    float scale_log2;                    // |scale| * log2(e)
+    uint32_t negate;                     // sign bits that the queries are flipped by: scale < 0
     float *part;                         // [2 * CTAs][tile][D + 2]
-    int stages;
 };
 
-// Bytes of one warp's ring stage: 16 tokens of K and V, and the two scales.
-__host__ __device__ constexpr int stage_bytes(int D) { return 2 * STEP * D + 16; }
+// Bytes of one warp's slots (a block of K and of V).
+__host__ __device__ constexpr int ring_bytes(int D) { return 2 * kv::BLOCK * D; }
 // Floats of one piece: maximum, sum and D values per query.
 __host__ __device__ constexpr int piece_floats(int tile, int D) { return tile * (D + 2); }
-__host__ __device__ inline size_t decode_smem(int tile, int D, int stages) {
-    return static_cast<size_t>(DEC_WARPS) * (static_cast<size_t>(stages) * stage_bytes(D) + piece_floats(tile, D) * 4);
+__host__ __device__ constexpr size_t decode_smem(int tile, int D, int warps) {
+    return static_cast<size_t>(warps) * (ring_bytes(D) + piece_floats(tile, D) * 4);
+}
+// Warps per CTA, one CTA an SM: registers allow 12 (8 with two MMA columns of
+// queries), shared memory fewer for wide tiles.
+constexpr int DEC_WARPS_1 = 12, DEC_WARPS_2 = 8;
+constexpr size_t DEC_SMEM = 226 * 1024;
+__host__ inline int decode_warps(int tile, int D) {
+    int warps = tile > 8 ? DEC_WARPS_2 : DEC_WARPS_1;
+    while (decode_smem(tile, D, warps) > DEC_SMEM) --warps;
+    return warps;
 }
 
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -83,12 +97,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Two codes, in bytes `lo` and `hi` of x (x = codes ^ 0x80), as fp16: 0x6400 + u
-// is 1024 + u, and 1024 + u - 1152 = u - 128, exactly.
+// Two codes as fp16, 1152 too large: their bytes of x = codes ^ 0x80 are picked
+// into the low bytes of 0x6400, 1024 + byte.
+constexpr float kCodeBias = 1152.0f;
 template <int kSel>
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t x) {
-    const uint32_t u = __byte_perm(x, 0x64646464u, kSel);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+__device__ __forceinline__ uint32_t biased_codes(uint32_t x) {
+    return __byte_perm(x, 0x64646464u, kSel);
+}
+// The same, exactly the codes.
+template <int kSel>
+__device__ __forceinline__ uint32_t exact_codes(uint32_t x) {
+    const uint32_t u = biased_codes<kSel>(x);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(kCodeBias));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
@@ -101,70 +121,172 @@ __device__ __forceinline__ int length_of(const DecodeParams &p, int b) {
     }
     return n;
 }
-__device__ __forceinline__ long long steps_of(const DecodeParams &p, int b) {      // of all its items
-    return static_cast<long long>((length_of(p, b) + STEP - 1) / STEP) * (p.c.H * p.GT);
-}
-__device__ __forceinline__ long long total_steps(const DecodeParams &p) {
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < p.B; b += 32) n += steps_of(p, b);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
-    return n;
-}
+// Where the steps of all items lie: sequence b's begin after those of the
+// sequences before it, H * GT items of item(len) steps each.  A lane keeps four
+// sequences' lengths of the first 128, which is all of them in most calls; more
+// are read again where they are needed.
+//
+// A warp takes about as long for one step of a block as for all four, so with at
+// least kCoarse blocks a warp every block counts whole and ranges are cut between
+// blocks; with fewer, ranges are cut between steps, so that more warps have work
+// (one sequence of 1000 tokens and 40 heads: 640 blocks, 2520 steps).
+struct Steps {
+    static constexpr int kCoarse = 4;
+    int len[4];
+    long long before;                    // steps of the sequences before this lane's four
+    long long total;
+    int warps;                           // of the grid
+    bool coarse;
 
-// A place in the order of steps: sequence b, item hg = h*GT + query tile, step.
-struct Place {
-    int b, hg, step, steps, len;
-    __device__ __forceinline__ void at(const DecodeParams &p, long long u) {
-        long long r = 0;
-        b = kv::find_item(u, p.B, &r, [&](int s) { return steps_of(p, s); });
-        len = length_of(p, b);
-        steps = (len + STEP - 1) / STEP;
-        hg = static_cast<int>(r / steps);
-        step = static_cast<int>(r % steps);
+    __device__ __forceinline__ int item(int n) const {
+        return coarse ? (n + kv::BLOCK - 1) / kv::BLOCK * SUBS : (n + STEP - 1) / STEP;
     }
-    // the next step; false past the last sequence
-    __device__ __forceinline__ bool next(const DecodeParams &p) {
-        if (++step < steps) return true;
-        step = 0;
-        if (++hg < p.c.H * p.GT) return true;
-        hg = 0;
-        do {
-            if (++b >= p.B) return false;
-            len = length_of(p, b);
-        } while (len == 0);
-        steps = (len + STEP - 1) / STEP;
-        return true;
+    __device__ __forceinline__ static void lengths(const DecodeParams &p, int b0, int (&n)[4]) {
+        const int b = b0 + 4 * (threadIdx.x & 31);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = b + j < p.B ? length_of(p, b + j) : 0;
+    }
+    __device__ __forceinline__ long long scan(const DecodeParams &p, const int (&n)[4], long long *prior) const {
+        const int lane = threadIdx.x & 31;
+        const long long mine = (static_cast<long long>(item(n[0])) + item(n[1]) + item(n[2]) + item(n[3])) * (p.c.H * p.GT);
+        long long sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        *prior = sum - mine;
+        return __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    __device__ __forceinline__ void sum(const DecodeParams &p) {
+        total = scan(p, len, &before);
+        for (int b0 = 128; b0 < p.B; b0 += 128) {
+            int n[4];
+            long long prior;
+            lengths(p, b0, n);
+            total += scan(p, n, &prior);
+        }
+    }
+    __device__ __forceinline__ void load(const DecodeParams &p, int grid_warps) {
+        warps = grid_warps;
+        lengths(p, 0, len);
+        coarse = true;
+        sum(p);
+        if (total < static_cast<long long>(kCoarse) * SUBS * warps) {
+            coarse = false;
+            sum(p);
+        }
+    }
+    // The first step of warp w's range.
+    __device__ __forceinline__ long long begin(int w) const {
+        return coarse ? total / SUBS * w / warps * SUBS : total * w / warps;
+    }
+    // The sequence (and its length), item and step of step u < total.
+    __device__ __forceinline__ void find(const DecodeParams &p, long long u, int *b, int *n, int *hg, int *step) const {
+        const int lane = threadIdx.x & 31;
+        const long long items = static_cast<long long>(p.c.H) * p.GT;
+        int v[4] = {len[0], len[1], len[2], len[3]};
+        long long prior = before, base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 128) {
+            if (b0) {
+                lengths(p, b0, v);
+                scan(p, v, &prior);
+            }
+            const long long mine = (static_cast<long long>(item(v[0])) + item(v[1]) + item(v[2]) + item(v[3])) * items;
+            long long r = u - base - prior;                          // within this lane's four sequences
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, r >= 0 && r < mine);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                int k = 0;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const long long c = item(v[j]) * items;
+                    if (k == j && r >= c) r -= c, k = j + 1;
+                }
+                const int own = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+                r = __shfl_sync(0xFFFFFFFFu, r, at);
+                *n = __shfl_sync(0xFFFFFFFFu, own, at);
+                *b = __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + k, at);
+                *hg = static_cast<int>(r / item(*n));
+                *step = static_cast<int>(r - static_cast<long long>(*hg) * item(*n));
+                return;
+            }
+            base += __shfl_sync(0xFFFFFFFFu, prior + mine, 31);
+        }
     }
 };
 
-// The block of a place, its table entry read ahead of the step that uses it; a
-// bad one (reported) reads block 0, which is always there.
+// What a warp works on next: steps [step, step + count) of the item (sequence b,
+// key/value head h, query tile gt), all in one block.
+struct Place {
+    int b, h, gt, step, count, steps, len;
+    __device__ __forceinline__ void at(const DecodeParams &p, const Steps &order, long long u) {
+        int hg;
+        order.find(p, u, &b, &len, &hg, &step);
+        steps = order.item(len);
+        h = hg / p.GT;
+        gt = hg % p.GT;
+    }
+    // the rest of the block that `step` lies in, of the item, and of the range
+    __device__ __forceinline__ void cut(long long left) {
+        count = min(SUBS - (step & (SUBS - 1)), steps - step);
+        if (left < count) count = static_cast<int>(left);
+    }
+    // the step after these; only called while the range has one
+    __device__ __forceinline__ void next(const DecodeParams &p, const Steps &order) {
+        step += count;
+        if (step < steps) return;
+        step = 0;
+        if (++gt < p.GT) return;
+        gt = 0;
+        if (++h < p.c.H) return;
+        h = 0;
+        do {
+            if (++b >= p.B) return;
+            len = length_of(p, b);
+        } while (len == 0);
+        steps = order.item(len);
+    }
+};
+
+// The block of a place; a bad number (reported) reads block 0, which is always there.
 __device__ __forceinline__ int page_at(const DecodeParams &p, const Place &w) {
-    const int page = kv::block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, w.b, w.step / (kv::BLOCK / STEP));
+    const int page = kv::block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, w.b, w.step / SUBS);
     return page < 0 ? 0 : page;
 }
 
+// The address of a place's block of K or V for its head.
 template <int D>
-__device__ __forceinline__ void issue_step(const DecodeParams &p, const Place &w, int page, uint32_t slot) {
+__device__ __forceinline__ const int8_t *block_codes(const DecodeParams &p, const Place &w, int page, int kv) {
+    return (kv ? p.c.codes[1] : p.c.codes[0]) + (static_cast<size_t>(page) * p.c.H + w.h) * (kv::BLOCK * D);
+}
+
+// Sub-tile j (16 tokens) of K and of V: this lane's bytes of it, in the order in
+// which they are read back.  K: rows (tokens) g and g + 8, 16 bytes at 16t of each
+// 64; V: rows 2t, 2t+1, 2t+8, 2t+9, the D/8 bytes at g*D/8.
+template <int D>
+__device__ __forceinline__ void issue_k(const int8_t *K, int j, uint32_t ring) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const size_t at = static_cast<size_t>(page) * p.c.H + w.hg / p.GT;
-    const size_t row0 = (at * kv::BLOCK + (w.step % (kv::BLOCK / STEP)) * STEP) * D;
-    const int8_t *K = p.c.codes[0] + row0, *V = p.c.codes[1] + row0;
-    uint32_t dst = slot + lane * 16;
+    const int8_t *src = K + (STEP * j + g) * D + 16 * t;
+    uint32_t dst = ring + j * (STEP * D) + lane * 16;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c, dst += 512) cp_async_16(dst, K + (g + 8 * r) * D + 64 * c + 16 * t, 16u);
-    if (D == 128) {
+        for (int c = 0; c < D / 64; ++c, dst += 512) cp_async_16(dst, src + 8 * r * D + 64 * c, 16u);
+}
+template <int D>
+__device__ __forceinline__ void issue_v(const int8_t *V, int j, uint32_t ring) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int8_t *src = V + (STEP * j + 2 * t) * D + g * (D / 8);
+    const uint32_t dst = ring + (SUBS + j) * (STEP * D) + lane * (D / 8);
 #pragma unroll
-        for (int k = 0; k < 4; ++k, dst += 512) cp_async_16(dst, V + (2 * t + (k & 1) + 8 * (k >> 1)) * D + 16 * g, 16u);
-    } else {
-        dst -= lane * 8;
-#pragma unroll
-        for (int k = 0; k < 4; ++k, dst += 256) cp_async_8(dst, V + (2 * t + (k & 1) + 8 * (k >> 1)) * D + 8 * g);
+    for (int k = 0; k < 4; ++k) {
+        const int8_t *s = src + ((k & 1) + 8 * (k >> 1)) * D;
+        if (D == 128)
+            cp_async_16(dst + k * 512, s, 16u);
+        else
+            cp_async_8(dst + k * 256, s);
     }
-    if (lane < 2) cp_async_4(slot + 2 * STEP * D + 4 * lane, (lane ? p.c.scale[1] : p.c.scale[0]) + at);
 }
 
 // One piece of an item in memory: per query its maximum (log2 units), its sum
@@ -174,14 +296,16 @@ __device__ __forceinline__ float *piece_row(float *piece, int q) { return piece 
 
 template <int D, int NT>
 struct State {
-    float acc[D / 16][NT][4];
-    float m[NT][2], l[NT][2];
+    float acc[D / 16][NT][4];            // in units of vs
+    float m[NT][2], l[NT][2];            // of this lane's queries 2t, 2t + 1: the same in all its g
+    float vs;                            // the scale acc is in (sV/127 of the last block with any)
+    float start[NT][2];                  // -1152 sum(Q): what a score starts at
     uint32_t q[D / 16][NT][2];
 
     // a new item: its queries (zero past the last one), nothing summed yet
     __device__ __forceinline__ void begin(const DecodeParams &p, const Place &w) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int h = w.hg / p.GT, q0 = (w.hg % p.GT) * p.tile;
+        const int h = w.h, q0 = w.gt * p.tile;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int qi = q0 + 8 * n + g;
@@ -194,9 +318,23 @@ struct State {
                 q[k][n][0] = v.x;
                 q[k][n][1] = v.y;
             }
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    q[k][n][r] ^= p.negate;
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&q[k][n][r]));
+                    sum += f.x + f.y;
+                }
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) start[n][e] = -kCodeBias * __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * e);
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.0f;
         }
+        vs = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -205,64 +343,126 @@ struct State {
                 for (int e = 0; e < 4; ++e) acc[k][n][e] = 0.0f;
     }
 
-    __device__ __forceinline__ void step(const DecodeParams &p, const Place &w, const uint8_t *slot) {
-        const int lane = threadIdx.x & 31, g = lane >> 2;
-        const uint8_t *mine = slot + lane * 16;
-        const float2 sc = *reinterpret_cast<const float2 *>(slot + 2 * STEP * D);
-        float x[NT][4];
+    // Scores of sub-tiles j and j + 1: rows are tokens g and g+8, a lane's four
+    // codes of a word are the MMA's columns 2t, 2t+1, 2t+8, 2t+9 (so are the
+    // queries').  Four chains of MMAs go side by side (two sub-tiles, two halves
+    // of each sum): a chain alone waits for each MMA's result.
+    __device__ __forceinline__ void scores(const uint8_t *ring, int j, float (&x)[2][NT][4]) const {
+        float y[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
-        // scores: rows are tokens g and g+8, a lane's four codes of a word are the
-        // MMA's columns 2t, 2t+1, 2t+8, 2t+9 (the queries' fragments follow suit)
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[s][n][e] = start[n][e & 1];
+                    y[s][n][e] = 0.0f;
+                }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-            const uint4 r0 = *reinterpret_cast<const uint4 *>(mine + 512 * c);
-            const uint4 r1 = *reinterpret_cast<const uint4 *>(mine + 512 * (D / 64 + c));
-            const uint32_t a[4] = {r0.x, r0.y, r0.z, r0.w}, b[4] = {r1.x, r1.y, r1.z, r1.w};
+            uint32_t a[2][4], b[2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t u = a[k] ^ 0x80808080u, v = b[k] ^ 0x80808080u;
-                const uint32_t a0 = codes_to_half2<0x4140>(u), a2 = codes_to_half2<0x4342>(u);
-                const uint32_t a1 = codes_to_half2<0x4140>(v), a3 = codes_to_half2<0x4342>(v);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816(x[n], a0, a1, a2, a3, q[4 * c + k][n][0], q[4 * c + k][n][1]);
+            for (int s = 0; s < 2; ++s) {
+                const uint8_t *mine = ring + (j + s) * (STEP * D) + (threadIdx.x & 31) * 16;
+                const uint4 r0 = *reinterpret_cast<const uint4 *>(mine + 512 * c);
+                const uint4 r1 = *reinterpret_cast<const uint4 *>(mine + 512 * (D / 64 + c));
+                a[s][0] = r0.x, a[s][1] = r0.y, a[s][2] = r0.z, a[s][3] = r0.w;
+                b[s][0] = r1.x, b[s][1] = r1.y, b[s][2] = r1.z, b[s][3] = r1.w;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t u = a[s][k] ^ 0x80808080u, v = b[s][k] ^ 0x80808080u;
+                    const uint32_t a0 = biased_codes<0x4140>(u), a2 = biased_codes<0x4342>(u);
+                    const uint32_t a1 = biased_codes<0x4140>(v), a3 = biased_codes<0x4342>(v);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816((k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, q[4 * c + k][n][0], q[4 * c + k][n][1]);
+                }
         }
-        const float ks = p.scale_log2 * (sc.x * (1.0f / 127.0f)), vs = sc.y * (1.0f / 127.0f);
-        const int t0 = w.step * STEP + g;
-        const bool in0 = t0 < w.len, in1 = t0 + 8 < w.len;
-        uint32_t b0[NT], b1[NT];
-        float alpha[NT][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[s][n][e] += y[s][n][e];
+    }
+
+    // The block's scores become weights (in `pf`, as the second product's
+    // fragments), the maxima and sums move on, and acc is rescaled to them and to
+    // the block's V scale.  Tokens outside [lo, hi) of the block weigh nothing.
+    __device__ __forceinline__ void weigh(const DecodeParams &p, float (&x)[SUBS / 2][2][NT][4], float sk, float sv, int lo,
+                                          int hi, uint32_t (&pf)[SUBS][NT][2]) {
+        const int g = (threadIdx.x & 31) >> 2;
+        const float ks = p.scale_log2 * (sk * (1.0f / 127.0f)), now = sv * (1.0f / 127.0f);
+        // a block whose scale is 0 stands for zeros, whatever its codes: values() is not called for it
+        const bool nothing = now == 0.0f;
+        const float turn = nothing ? 1.0f : vs / now;
+        if (!nothing) vs = now;
+        const bool cut = lo > 0 || hi < kv::BLOCK;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float pr[4];
+            float keep[2], alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float u = in0 ? x[n][e] * ks : -INFINITY, v = in1 ? x[n][2 + e] * ks : -INFINITY;
-                float top = fmaxf(u, v);
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < SUBS; ++j) {
+                    float &u = x[j >> 1][j & 1][n][e], &v = x[j >> 1][j & 1][n][2 + e];
+                    if (cut) {
+                        const int t0 = STEP * j + g;
+                        u = t0 >= lo && t0 < hi ? u : -INFINITY;
+                        v = t0 + 8 >= lo && t0 + 8 < hi ? v : -INFINITY;
+                    }
+                    top = fmaxf(top, fmaxf(u, v));
+                }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                top = fmaxf(top, m[n][e]);
-                alpha[n][e] = ex2(m[n][e] - top);
-                m[n][e] = top;
-                pr[e] = ex2(u - top);
-                pr[2 + e] = ex2(v - top);
-                l[n][e] = fmaf(l[n][e], alpha[n][e], pr[e] + pr[2 + e]);
+                const float to = fmaxf(top * ks, m[n][e]);
+                alpha[e] = ex2(m[n][e] - to);
+                m[n][e] = to;
+#pragma unroll
+                for (int j = 0; j < SUBS; ++j) {
+                    float &u = x[j >> 1][j & 1][n][e], &v = x[j >> 1][j & 1][n][2 + e];
+                    const bool in0 = !cut || u != -INFINITY, in1 = !cut || v != -INFINITY;
+                    u = in0 ? ex2(fmaf(u, ks, -to)) : 0.0f;
+                    v = in1 ? ex2(fmaf(v, ks, -to)) : 0.0f;
+                }
+                keep[e] = alpha[e] * turn;
             }
-            const __half2 h0 = __floats2half2_rn(pr[0], pr[1]), h1 = __floats2half2_rn(pr[2], pr[3]);
-            b0[n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h0));
-            b1[n] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h1));
+            // the weights' sum over the block's tokens, the same in every row of the MMA's result
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            constexpr uint32_t kOnes = 0x3C003C00u;
+#pragma unroll
+            for (int j = 0; j < SUBS; ++j) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const __half2 h = __floats2half2_rn(x[j >> 1][j & 1][n][2 * r], x[j >> 1][j & 1][n][2 * r + 1]);
+                    pf[j][n][r] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
+                }
+                mma16816(sum, kOnes, kOnes, kOnes, kOnes, pf[j][n][0], pf[j][n][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l[n][e] = fmaf(l[n][e], alpha[e], sum[e]);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[k][n][e] *= keep[e & 1];
         }
-        // values: rows are columns d of V, two per lane and MMA; k is the token
-        const uint8_t *vsrc = slot + STEP * D + lane * (D / 8);
+    }
+
+    // Sub-tile j's values: rows are columns d of V, two per lane and MMA; k is the token.
+    __device__ __forceinline__ void values(const uint8_t *ring, int j, const uint32_t (&pf)[NT][2]) {
+        const uint8_t *mine = ring + (SUBS + j) * (STEP * D) + (threadIdx.x & 31) * (D / 8);
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (D == 128) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(vsrc + 512 * k);
+                const uint4 r = *reinterpret_cast<const uint4 *>(mine + 512 * k);
                 v[k][0] = r.x, v[k][1] = r.y, v[k][D / 32 - 2] = r.z, v[k][D / 32 - 1] = r.w;
             } else {
-                const uint2 r = *reinterpret_cast<const uint2 *>(vsrc + 256 * k);
+                const uint2 r = *reinterpret_cast<const uint2 *>(mine + 256 * k);
                 v[k][0] = r.x, v[k][1] = r.y;
             }
         }
@@ -274,16 +474,10 @@ struct State {
             for (int half = 0; half < 2; ++half) {
                 const uint32_t lo = half ? __byte_perm(v[0][i], v[1][i], 0x7362) : __byte_perm(v[0][i], v[1][i], 0x5140);
                 const uint32_t hi = half ? __byte_perm(v[2][i], v[3][i], 0x7362) : __byte_perm(v[2][i], v[3][i], 0x5140);
-                const uint32_t a0 = codes_to_half2<0x4140>(lo), a1 = codes_to_half2<0x4342>(lo);
-                const uint32_t a2 = codes_to_half2<0x4140>(hi), a3 = codes_to_half2<0x4342>(hi);
+                const uint32_t a0 = exact_codes<0x4140>(lo), a1 = exact_codes<0x4342>(lo);
+                const uint32_t a2 = exact_codes<0x4140>(hi), a3 = exact_codes<0x4342>(hi);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816(part, a0, a1, a2, a3, b0[n], b1[n]);
-                    float(&o)[4] = acc[2 * i + half][n];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[e] = fmaf(part[e], vs, o[e] * alpha[n][e & 1]);
-                }
+                for (int n = 0; n < NT; ++n) mma16816(acc[2 * i + half][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
             }
         }
     }
@@ -291,21 +485,19 @@ struct State {
     // The item's output, or its piece.
     __device__ __forceinline__ void end(const DecodeParams &p, const Place &w, bool whole, float *piece) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int h = w.hg / p.GT, q0 = (w.hg % p.GT) * p.tile;
+        const int h = w.h, q0 = w.gt * p.tile;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[n][e];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                const float sum = l[n][e];
                 const int qi = 8 * n + 2 * t + e;
                 if (qi >= p.tile || q0 + qi >= p.G) continue;
                 if (whole) {
-                    const float inv = 1.0f / sum;
+                    const float f = vs / sum;
                     __half2 o[D / 16];
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) o[k] = __floats2half2_rn(acc[k][n][e] * inv, acc[k][n][2 + e] * inv);
+                    for (int k = 0; k < D / 16; ++k) o[k] = __floats2half2_rn(acc[k][n][e] * f, acc[k][n][2 + e] * f);
                     __half *dst = p.O + static_cast<size_t>(w.b) * p.ldo + static_cast<size_t>(h * p.G + q0 + qi) * D +
                                   g * (D / 8);
 #pragma unroll
@@ -320,7 +512,7 @@ struct State {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         *reinterpret_cast<float2 *>(row + 2 + g * (D / 8) + 2 * k) =
-                            make_float2(acc[k][n][e], acc[k][n][2 + e]);
+                            make_float2(acc[k][n][e] * vs, acc[k][n][2 + e] * vs);
                 }
             }
     }
@@ -328,85 +520,120 @@ struct State {
 
 // What a warp left of an item it did not do alone.
 struct Piece {
-    int b, hg;                           // b < 0: none
+    int b, h, gt;                        // b < 0: none
     bool starts, ends;                   // the piece holds the item's first / last step
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
     attention_decode_kernel(const __grid_constant__ DecodeParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Piece pieces[2 * DEC_WARPS];
+    __shared__ Piece pieces[2 * DEC_WARPS_1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int warp_ring = p.stages * stage_bytes(D);
-    uint8_t *ring = smem + warp * warp_ring;
+    const int cta_warps = blockDim.x >> 5;
+    uint8_t *ring = smem + warp * ring_bytes(D);
     const uint32_t ring_u = smem_u32(ring);
-    // a warp's first piece is written while its ring is still in use, its last one into the ring
-    float *firsts = reinterpret_cast<float *>(smem + DEC_WARPS * warp_ring);
-    if (threadIdx.x < 2 * DEC_WARPS) pieces[threadIdx.x].b = -1;
-    // sequences without tokens
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (length_of(p, b) == 0)
-            for (int i = threadIdx.x; i < p.c.H * p.G * (D / 8); i += DEC_THREADS)
-                *reinterpret_cast<uint4 *>(p.O + static_cast<size_t>(b) * p.ldo + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
+    // a warp's first piece is written while its slots are still in use, its last one into them
+    float *firsts = reinterpret_cast<float *>(smem + cta_warps * ring_bytes(D));
+    if (lane < 2) pieces[2 * warp + lane].b = -1;
+    __syncwarp();
+    griddep_launch_dependents();         // combine_kernel may find its items meanwhile (it fits in beside no CTA of this grid)
 
-    const long long S = total_steps(p);
-    const int warps = gridDim.x * DEC_WARPS, me = blockIdx.x * DEC_WARPS + warp;
-    const long long u0 = decode::unit_begin(S, me, warps), u1 = decode::unit_begin(S, me + 1, warps);
+    Steps order;
+    order.load(p, gridDim.x * cta_warps);
+    const int me = blockIdx.x * cta_warps + warp;
+    const long long u0 = order.begin(me), u1 = order.begin(me + 1);
     if (u0 < u1) {
-        Place w, ahead;
-        w.at(p, u0);
-        ahead = w;
-        long long issued = u0;
-        int page = page_at(p, ahead);
-        int fill = 0;
-        auto issue = [&]() {
-            if (issued < u1) {
-                issue_step<D>(p, ahead, page, ring_u + fill * stage_bytes(D));
-                if (++issued < u1) {
-                    ahead.next(p);
-                    page = page_at(p, ahead);
-                }
+        Place w;
+        w.at(p, order, u0);
+        w.cut(u1 - u0);
+        int page = page_at(p, w);
+        {
+            const int8_t *K = block_codes<D>(p, w, page, 0), *V = block_codes<D>(p, w, page, 1);
+            const int j0 = w.step & (SUBS - 1), j1 = j0 + w.count;
+#pragma unroll
+            for (int j = 0; j < SUBS; ++j) {
+                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
+                if (j & 1) cp_async_commit();
             }
-            cp_async_commit();
-            if (++fill == p.stages) fill = 0;
-        };
-        for (int s = 0; s + 1 < p.stages; ++s) issue();
+#pragma unroll
+            for (int j = 0; j < SUBS; ++j) {
+                if (j >= j0 && j < j1) issue_v<D>(V, j, ring_u);
+                if (j & 1) cp_async_commit();
+            }
+        }
+        size_t at = static_cast<size_t>(page) * p.c.H + w.h;
+        float sk = __ldg(p.c.scale[0] + at), sv = __ldg(p.c.scale[1] + at);
         State<D, NT> st;
         st.begin(p, w);
+        long long done = u0 + w.count;               // steps of the range up to the end of w
+        Place ahead = w;
+        if (done < u1) {
+            ahead.next(p, order);
+            ahead.cut(u1 - done);
+            page = page_at(p, ahead);
+        }
         bool starts = w.step == 0, first = true;
-        int slot = 0;
-        for (long long u = u0; u < u1; ++u) {
-            if (p.stages == 2)
-                cp_async_wait<0>();
-            else if (p.stages == 3)
-                cp_async_wait<1>();
-            else
-                cp_async_wait<2>();
-            __syncwarp();                       // lanes 0 and 1 copied the scales; the slot read last is free
-            issue();
-            st.step(p, w, ring + slot * stage_bytes(D));
-            if (++slot == p.stages) slot = 0;
-            const bool ends = w.step + 1 == w.steps;
-            if (ends || u + 1 == u1) {
+        while (true) {
+            // the block after this one: its scales now, its codes as the slots come free
+            const bool more = done < u1;
+            const int8_t *K = nullptr, *V = nullptr;
+            float sk_next = 0.0f, sv_next = 0.0f;
+            int j0 = SUBS, j1 = 0;
+            if (more) {
+                K = block_codes<D>(p, ahead, page, 0);
+                V = block_codes<D>(p, ahead, page, 1);
+                at = static_cast<size_t>(page) * p.c.H + ahead.h;
+                sk_next = __ldg(p.c.scale[0] + at);
+                sv_next = __ldg(p.c.scale[1] + at);
+                j0 = ahead.step & (SUBS - 1);
+                j1 = j0 + ahead.count;
+            }
+            float x[SUBS / 2][2][NT][4];
+#pragma unroll
+            for (int j = 0; j < SUBS; j += 2) {
+                cp_async_wait<SUBS - 1>();
+                st.scores(ring, j, x[j / 2]);
+                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
+                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
+                cp_async_commit();
+            }
+            const int lo = (w.step & (SUBS - 1)) * STEP;
+            const int hi = min(lo + w.count * STEP, w.len - w.step / SUBS * kv::BLOCK);
+            uint32_t pf[SUBS][NT][2];
+            st.weigh(p, x, sk, sv, lo, hi, pf);
+#pragma unroll
+            for (int j = 0; j < SUBS; j += 2) {
+                cp_async_wait<SUBS - 1>();
+                if (sv != 0.0f) {
+                    st.values(ring, j, pf[j]);
+                    st.values(ring, j + 1, pf[j + 1]);
+                }
+                if (j >= j0 && j < j1) issue_v<D>(V, j, ring_u);
+                if (j + 1 >= j0 && j + 1 < j1) issue_v<D>(V, j + 1, ring_u);
+                cp_async_commit();
+            }
+            const bool ends = w.step + w.count == w.steps;
+            if (ends || !more) {
                 const bool whole = starts && ends;
                 if (!whole) {
-                    if (!first) {
-                        cp_async_wait<0>();     // nothing of the ring is in flight or unread
-                        __syncwarp();
-                    }
-                    if (lane == 0) pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.hg, starts, ends};
+                    if (!first) __syncwarp();        // the range's last steps: every lane has read its slots
+                    if (lane == 0) pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.h, w.gt, starts, ends};
                 }
                 st.end(p, w, whole, first ? firsts + warp * piece_floats(p.tile, D) : reinterpret_cast<float *>(ring));
                 first = false;
-                if (u + 1 < u1) {
-                    w.next(p);
-                    st.begin(p, w);
-                    starts = true;
-                }
-            } else {
-                w.next(p);
+                starts = true;
+                if (more) st.begin(p, ahead);
+            }
+            if (!more) break;
+            w = ahead;
+            sk = sk_next;
+            sv = sv_next;
+            done += w.count;
+            if (done < u1) {
+                ahead.next(p, order);
+                ahead.cut(u1 - done);
+                page = page_at(p, ahead);
             }
         }
     }
@@ -415,41 +642,39 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 2 : 1)
     // Merge this CTA's pieces, item by item in order; an item that begins or ends
     // in another CTA leaves one piece for combine_kernel, in slot 0 if it begins
     // where the CTA's range does, else in slot 1.
-    const long long U0 = decode::unit_begin(S, blockIdx.x * DEC_WARPS, warps);
-    for (int i = 0; i < 2 * DEC_WARPS;) {
+    const long long U0 = order.begin(blockIdx.x * cta_warps);
+    auto piece_of = [&](int k) {
+        return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * ring_bytes(D))
+                       : firsts + (k >> 1) * piece_floats(p.tile, D);
+    };
+    for (int i = 0; i < 2 * cta_warps;) {
         const Piece a = pieces[i];
         if (a.b < 0) {
             ++i;
             continue;
         }
         int j = i + 1, last = i;
-        for (; j < 2 * DEC_WARPS; ++j) {
+        for (; j < 2 * cta_warps; ++j) {
             if (pieces[j].b < 0) continue;
-            if (pieces[j].b != a.b || pieces[j].hg != a.hg) break;
+            if (pieces[j].b != a.b || pieces[j].h != a.h || pieces[j].gt != a.gt) break;
             last = j;
         }
         const bool whole = a.starts && pieces[last].ends;
-        const int first_warp = blockIdx.x * DEC_WARPS + (i >> 1);
-        const int out_slot = ((i & 1) == 0 && decode::unit_begin(S, first_warp, warps) == U0) ? 0 : 1;
+        const int first_warp = blockIdx.x * cta_warps + (i >> 1);
+        const int out_slot = ((i & 1) == 0 && order.begin(first_warp) == U0) ? 0 : 1;
         float *out = p.part + static_cast<size_t>(2 * blockIdx.x + out_slot) * piece_floats(p.tile, D);
-        const int h = a.hg / p.GT, q0 = (a.hg % p.GT) * p.tile;
+        const int h = a.h, q0 = a.gt * p.tile;
         const int nq = min(p.tile, p.G - q0);
-        for (int e = threadIdx.x; e < nq * (D / 2); e += DEC_THREADS) {
+        for (int e = threadIdx.x; e < nq * (D / 2); e += blockDim.x) {
             const int q = e / (D / 2), d = 2 * (e % (D / 2));
             float top = -INFINITY;
-            for (int k = i; k <= last; ++k) {
-                if (pieces[k].b < 0) continue;
-                float *src = (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)
-                                     : firsts + (k >> 1) * piece_floats(p.tile, D);
-                top = fmaxf(top, piece_row<D>(src, q)[0]);
-            }
+            for (int k = i; k <= last; ++k)
+                if (pieces[k].b >= 0) top = fmaxf(top, piece_row<D>(piece_of(k), q)[0]);
             float sum = 0.0f;
             float2 o = make_float2(0.0f, 0.0f);
             for (int k = i; k <= last; ++k) {
                 if (pieces[k].b < 0) continue;
-                float *src = (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)
-                                     : firsts + (k >> 1) * piece_floats(p.tile, D);
-                const float *row = piece_row<D>(src, q);
+                const float *row = piece_row<D>(piece_of(k), q);
                 const float wgt = ex2(row[0] - top);
                 const float2 v = *reinterpret_cast<const float2 *>(row + 2 + d);
                 sum = fmaf(wgt, row[1], sum);
@@ -472,40 +697,47 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 2 : 1)
         }
         i = j;
     }
+    // sequences without tokens
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (length_of(p, b) == 0)
+            for (int i = threadIdx.x; i < p.c.H * p.G * (D / 8); i += blockDim.x)
+                *reinterpret_cast<uint4 *>(p.O + static_cast<size_t>(b) * p.ldo + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // The items that cross CTAs.  Block (c, q): if the range of CTA c + 1 begins
 // inside an item that began in CTA c's range, that item's query q is the sum of
 // the pieces of CTAs c, c + 1, ... up to the one where it ends.  One thread per
-// value; the pieces are read in order, eight ahead.
+// value; the pieces are read in order, eight at a time.  Launched as a
+// programmatic dependent: which item it is, is known from the lengths alone.
 template <int D>
-__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas) {
-    griddep_wait();
+__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas, int cta_warps) {
     const int c = blockIdx.x, q = blockIdx.y, d = threadIdx.x;
-    const long long S = total_steps(p);
-    const int warps = ctas * DEC_WARPS;
-    auto begin = [&](int cta) { return decode::unit_begin(S, cta * DEC_WARPS, warps); };
+    Steps order;
+    order.load(p, ctas * cta_warps);
+    auto begin = [&](int cta) { return order.begin(cta * cta_warps); };
     const long long u = begin(c + 1);
-    if (u >= S || u == begin(c)) return;
     Place w;
-    w.at(p, u);
+    w.step = w.steps = w.gt = 0;
+    if (u < order.total) w.at(p, order, u);
+    // every block waits, also one without an item: the kernels after this one in
+    // the stream wait for this grid alone
+    griddep_wait();
     const long long start = u - w.step, end = start + w.steps;
-    const int q0 = (w.hg % p.GT) * p.tile;
+    const int q0 = w.gt * p.tile;
     if (w.step == 0 || start < begin(c) || q0 + q >= p.G) return;
-    const int last = decode::unit_owner(S, end - 1, warps) / DEC_WARPS;
     auto row = [&](int cta) {
         const int slot = start <= begin(cta) ? 0 : 1;
         return piece_row<D>(p.part + static_cast<size_t>(2 * cta + slot) * piece_floats(p.tile, D), q);
     };
     float top = -INFINITY, sum = 0.0f, o = 0.0f;
-    for (int k0 = c; k0 <= last; k0 += 8) {
+    for (int k0 = c; k0 < ctas && begin(k0) < end; k0 += 8) {
         float m[8], l[8], v[8], was = top;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             m[k] = -INFINITY;
             l[k] = v[k] = 0.0f;
             // a CTA without steps (fewer steps than warps) has no piece
-            if (k0 + k <= last && begin(k0 + k) < begin(k0 + k + 1)) {
+            if (k0 + k < ctas && begin(k0 + k) < min(end, begin(k0 + k + 1))) {
                 const float *r = row(k0 + k);
                 m[k] = __ldcg(r);
                 l[k] = __ldcg(r + 1);
@@ -524,8 +756,7 @@ __global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_const
             o = fmaf(wgt, v[k], o);
         }
     }
-    const int h = w.hg / p.GT;
-    p.O[static_cast<size_t>(w.b) * p.ldo + static_cast<size_t>(h * p.G + q0 + q) * D + d] = __float2half_rn(o / sum);
+    p.O[static_cast<size_t>(w.b) * p.ldo + static_cast<size_t>(w.h * p.G + q0 + q) * D + d] = __float2half_rn(o / sum);
 }
 
 }  // namespace attn

@@ -489,25 +489,52 @@ struct Epilogue {
     bool any() const { return bias || residual || act != I8R_ACT_NONE; }
 };
 
-// relu keeps NaN (a comparison, not fmaxf).  gelu is y * Phi(y) with Phi from
-// erfcf, whose relative error stays small in the left tail where 1 + erff
-// cancels.
-__device__ __forceinline__ float activate(float y, int act) {
-    if (act == I8R_ACT_RELU) return y < 0.0f ? 0.0f : y;
-    if (act == I8R_ACT_GELU) return 0.5f * y * erfcf(-0.70710678f * y);
-    return y;
+__device__ __forceinline__ float relu(float y) { return y < 0.0f ? 0.0f : y; }      // NaN stays
+
+// gelu(y) = y Phi(y) = max(y, 0) - |y| Phi(-|y|), where Phi(-a) = erfc(a/sqrt(2))/2
+// = e^(-a^2/2) erfcx(a/sqrt(2))/2 and erfcx is close to a rational function:
+// with t = 1/(1 + 0.2616295 a), erfcx(a/sqrt(2))/2 = t P(t), P of degree 6,
+// fitted by reweighted least squares to a relative error of 3.9e-7 over
+// a/sqrt(2) in [0, 8] (and the product underflows past it).  No cancellation in
+// either tail, and about 15 instructions: with erfcf the 13B fc1 prompt took
+// 360 us for 173 without an epilogue, the epilogue warps falling behind the MMAs.
+__device__ __forceinline__ float gelu(float y) {
+    const float a = fminf(fabsf(y), 30.0f);             // infinity: no 0 * inf; a NaN stays in relu(y)
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(a, 0.26162951f, 1.0f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * a * -0.72134752f));
+    float s = fmaf(-0.07287046f, t, 0.22363427f);
+    s = fmaf(s, t, -0.10171863f);
+    s = fmaf(s, t, 0.16510032f);
+    s = fmaf(s, t, 0.07372782f);
+    s = fmaf(s, t, 0.10798129f);
+    s = fmaf(s, t, 0.10414525f);
+    return fmaf(-a, s * t * e, relu(y));
 }
 
-// The epilogue of eight neighbouring columns: b8 and r8 hold eight fp16 of the
-// bias and the residual (zero where the call has none).
-__device__ __forceinline__ void apply_epilogue8(float (&y)[8], const uint4 &b8, const uint4 &r8, int act) {
-    const __half2 *b = reinterpret_cast<const __half2 *>(&b8);
+// The epilogue of eight neighbouring columns: their bias in fp32, and eight fp16
+// of the residual (both read only where the call has them; the branches are the
+// same for the whole grid).
+__device__ __forceinline__ void apply_epilogue8(float (&y)[8], const float *bias, const uint4 &r8, const Epilogue &epi) {
     const __half2 *r = reinterpret_cast<const __half2 *>(&r8);
+    if (epi.bias) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 bf = __half22float2(b[e]), rf = __half22float2(r[e]);
-        y[2 * e] = activate(y[2 * e] + bf.x, act) + rf.x;
-        y[2 * e + 1] = activate(y[2 * e + 1] + bf.y, act) + rf.y;
+        for (int e = 0; e < 8; ++e) y[e] += bias[e];
+    }
+    if (epi.act == I8R_ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = relu(y[e]);
+    } else if (epi.act == I8R_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = gelu(y[e]);
+    }
+    if (epi.residual) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(r[e]);
+            y[2 * e] += f.x;
+            y[2 * e + 1] += f.y;
+        }
     }
 }
 

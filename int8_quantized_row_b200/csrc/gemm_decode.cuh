@@ -187,7 +187,17 @@ __global__ void __launch_bounds__(256) decode_finalize_kernel(const int32_t *__r
     float yf[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) yf[e] = fmaf(static_cast<float>(av[e]), rs * wv[e], ov[e]);
-    if (kEpi) apply_epilogue8(yf, b8, r8, epi.act);
+    if (kEpi) {
+        float bias[8];
+        const __half2 *h = reinterpret_cast<const __half2 *>(&b8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(h[e]);
+            bias[2 * e] = f.x;
+            bias[2 * e + 1] = f.y;
+        }
+        apply_epilogue8(yf, bias, r8, epi);
+    }
     __align__(16) __half y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __float2half_rn(yf[e]);

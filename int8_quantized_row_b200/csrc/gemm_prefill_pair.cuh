@@ -31,7 +31,8 @@
 //                  the W16 rows of the outlier columns arrive as one-row loads.
 //   empty[s]       each CTA's own; the leader's MMA commit arrives on both
 //   acc_int_full, acc_final_full  each CTA's own; committed to both
-//   acc_conv, acc_empty           leader's, 8 arrivals (4 epilogue warps x 2)
+//   acc_conv, acc_empty           leader's, 8 arrivals (4 epilogue warps x 2; 16 from
+//                  the 8 of the fused epilogue)
 // Every wait is bounded (timeout -> device status word, abort flag); both
 // CTAs always reach the final cluster barrier.
 #pragma once
@@ -53,7 +54,8 @@ constexpr int B_BYTES = 128 * BK;          // 32 KB: this CTA's 128 columns
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int XO_BYTES = 128 * OBK * 2;    // 16 KB: an outlier stage's Xo rows
 constexpr int B_CHUNK_F16 = 64 * OBK * 2;  // 64 columns x 64 outlier rows, fp16
-constexpr int THREADS = 192;
+constexpr int THREADS = 192;               // producer, MMA issuer, four epilogue warps
+constexpr int THREADS_EPI = 320;           // with the fused epilogue: eight of them, half of the columns each
 constexpr int TMEM_COLS = 512;
 constexpr int kDefer = 4;
 
@@ -61,7 +63,11 @@ constexpr int EPI_SW_BYTES = BN * 4;
 constexpr int EPI_STAGE_BYTES = 32 * 32 * 2;
 constexpr int EPI_WARP_BYTES = EPI_SW_BYTES + 2 * EPI_STAGE_BYTES;
 constexpr int EPI_BYTES = 4 * EPI_WARP_BYTES;
+// With the fused epilogue, per warp: sW and the bias of its 128 columns, a 32 x 32 block.
+constexpr int EPI_FUSED_WARP_BYTES = 2 * (BN / 2) * 4 + EPI_STAGE_BYTES;
+constexpr int EPI_FUSED_BYTES = 8 * EPI_FUSED_WARP_BYTES;
 constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + 512;
+constexpr size_t SMEM_BYTES_FUSED = 1024 + STAGES * STAGE_BYTES + EPI_FUSED_BYTES + 512;
 
 struct Params {
     int T, K, N;
@@ -118,10 +124,14 @@ __device__ __forceinline__ bool walk_schedule(const Params &p, int nob, int clus
 }
 
 // kS32: int32 accumulators out.  kEpi: Y with the fused epilogue (bias,
-// activation, residual); its own instance, so that the plain layer's epilogue
-// stays as it is.
+// activation, residual), its own instance, so that the plain layer's kernel stays
+// as it is.  The layer is bound by operand tiles out of L2 (13B fc1, 2048 rows:
+// 1.7 GB in about 173 us), so the residual and Y cross L2 in whole sectors (rows
+// through a 32 x 32 block in shared memory; 16-byte pieces a lane's row at a time
+// cost 20 us for Y and 50 us for the residual), and eight epilogue warps, half of
+// the columns each, keep the conversion out of the way.
 template <bool kS32, bool kEpi>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(kEpi ? THREADS_EPI : THREADS, 1)
     gemm_prefill_pair_kernel(const __grid_constant__ CUtensorMap map_xq, const __grid_constant__ CUtensorMap map_wq,
                              const __grid_constant__ CUtensorMap map_xo, const __grid_constant__ CUtensorMap map_w16,
                              const __grid_constant__ CUtensorMap map_w16x4, const __grid_constant__ CUtensorMap map_w16o,
@@ -129,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *epi = smem + STAGES * STAGE_BYTES;
-    Barriers *bars = reinterpret_cast<Barriers *>(epi + EPI_BYTES);
+    Barriers *bars = reinterpret_cast<Barriers *>(epi + (kEpi ? EPI_FUSED_BYTES : EPI_BYTES));
     volatile int *abort = &bars->abort;
 
     const int warp = threadIdx.x >> 5;
@@ -146,9 +156,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_int_full[b], 1);
-            mbar_init(&bars->acc_conv[b], 8);
+            mbar_init(&bars->acc_conv[b], kEpi ? 16 : 8);
             mbar_init(&bars->acc_final_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 8);
+            mbar_init(&bars->acc_empty[b], kEpi ? 16 : 8);
         }
         mbar_init(&bars->drain, 1);
         for (int s = 0; s < STAGES; ++s) mbar_init(&bars->wq_ready[s], 2);
@@ -402,8 +412,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
-        uint8_t *mine = epi + (warp - 2) * EPI_WARP_BYTES;
-        float *sw_s = reinterpret_cast<float *>(mine);
+        uint8_t *mine = epi + (warp - 2) * (kEpi ? EPI_FUSED_WARP_BYTES : EPI_WARP_BYTES);
+        // this warp's 32-column chunks of the tile
+        const int c_first = kEpi ? (warp - 2) / 4 * (BN / 64) : 0;
+        const int c_end = kEpi ? c_first + BN / 64 : BN / 32;
+        float *sw_s = reinterpret_cast<float *>(mine) - c_first * 32;      // indexed by the tile's column
+        float *bias_s = sw_s + BN / 2;
         uint8_t *stage_s = mine + EPI_SW_BYTES;
         int chunk_seq = 0;
         int it = 0;
@@ -417,32 +431,52 @@ __global__ void __launch_bounds__(THREADS, 1)
             float rs = 0.0f;
             if (!kS32) {
                 rs = row_ok ? p.sX[t] * (1.0f / 16129.0f) : 0.0f;
-                const int nl = n0 + lane * 8;
-                float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-                if (nl < p.N) {
-                    s0 = __ldg(reinterpret_cast<const float4 *>(p.sW + nl));
-                    s1 = __ldg(reinterpret_cast<const float4 *>(p.sW + nl + 4));
+                if (!kEpi) {
+                    const int nl = n0 + lane * 8;
+                    float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+                    if (nl < p.N) {
+                        s0 = __ldg(reinterpret_cast<const float4 *>(p.sW + nl));
+                        s1 = __ldg(reinterpret_cast<const float4 *>(p.sW + nl + 4));
+                    }
+                    __syncwarp();
+                    reinterpret_cast<float4 *>(sw_s)[lane * 2] = s0;
+                    reinterpret_cast<float4 *>(sw_s)[lane * 2 + 1] = s1;
+                    __syncwarp();
+                } else {
+                    const int c = c_first * 32 + lane * 4, nl = n0 + c;
+                    float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float2 b0 = make_float2(0.f, 0.f), b1 = b0;
+                    if (nl < p.N) {
+                        s0 = __ldg(reinterpret_cast<const float4 *>(p.sW + nl));
+                        if (p.epi.bias) {
+                            const uint2 h = __ldg(reinterpret_cast<const uint2 *>(p.epi.bias + nl));
+                            b0 = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
+                            b1 = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
+                        }
+                    }
+                    __syncwarp();
+                    *reinterpret_cast<float4 *>(sw_s + c) = s0;
+                    *reinterpret_cast<float4 *>(bias_s + c) = make_float4(b0.x, b0.y, b1.x, b1.y);
+                    __syncwarp();
                 }
-                __syncwarp();
-                reinterpret_cast<float4 *>(sw_s)[lane * 2] = s0;
-                reinterpret_cast<float4 *>(sw_s)[lane * 2 + 1] = s1;
-                __syncwarp();
             }
-            // Fused epilogue: the residual of a 32-column chunk (64 bytes of this
-            // lane's row) and its bias are requested one chunk ahead, the first
-            // chunk's before the accumulator is waited for.
-            uint4 res[4], bia[4];
-            auto fetch = [&](int c) {
+            // Fused epilogue: the residual is asked for two chunks ahead, the first ones
+            // before the accumulator is waited for.  Instruction k of a chunk reads rows 8k .. 8k+7 of the warp's
+            // 32, 64 bytes each: this lane row 8k + lane/4, columns 8 (lane%4) ..
+            const int sub_row = m0 + quad * 32 + (lane >> 2), sub_col = n0 + c_first * 32 + (lane & 3) * 8;
+            uint4 res[2][4];
+            auto fetch = [&](int i) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + c * 32 + g * 8;
-                    res[g] = bia[g] = make_uint4(0u, 0u, 0u, 0u);
-                    if (n < p.N && p.epi.bias) bia[g] = __ldg(reinterpret_cast<const uint4 *>(p.epi.bias + n));
-                    if (n < p.N && row_ok && p.epi.residual)
-                        res[g] = __ldcg(reinterpret_cast<const uint4 *>(p.epi.residual + static_cast<size_t>(t) * p.N + n));
-                }
+                for (int k = 0; k < 4; ++k)
+                    res[i & 1][k] = sub_col + 32 * i < p.N && sub_row + 8 * k < p.T
+                                        ? __ldcg(reinterpret_cast<const uint4 *>(
+                                              p.epi.residual + static_cast<size_t>(sub_row + 8 * k) * p.N + sub_col + 32 * i))
+                                        : make_uint4(0u, 0u, 0u, 0u);
             };
-            if (kEpi) fetch(0);
+            if (kEpi && p.epi.residual) {
+                fetch(0);
+                fetch(1);
+            }
             if (!warp_wait(&bars->acc_int_full[buf], use, abort, I8R_DEV_TMEM_TIMEOUT)) break;
             tc_fence_after_sync();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * BN);
@@ -466,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             } else {
                 if (nob) {
 #pragma unroll 1
-                    for (int c = 0; c < BN / 32; ++c) {
+                    for (int c = c_first; c < c_end; ++c) {
                         uint32_t r[32];
                         tmem_ld32(taddr + c * 32, r);
                         tmem_wait_ld();
@@ -482,32 +516,78 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!warp_wait(&bars->acc_final_full[buf], use, abort, I8R_DEV_TMEM_TIMEOUT)) break;
                     tc_fence_after_sync();
                 }
+                if constexpr (kEpi) {
+                    // Chunk c + 1 is on its way from tensor memory while chunk c is worked
+                    // on.  The block holds row r's four 16-byte pieces in places q ^ (r/2 % 4):
+                    // no bank conflicts by rows or by pieces.
+                    uint32_t r[2][32];
+                    uint4 *own = reinterpret_cast<uint4 *>(stage_s + lane * 64);
+                    const int own_x = (lane >> 1) & 3;
+                    uint4 *sub = reinterpret_cast<uint4 *>(stage_s + (lane >> 2) * 64) + ((lane & 3) ^ ((lane >> 3) & 3));
+                    tmem_ld32(taddr + c_first * 32, r[0]);
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i) {
+                        const int c = c_first + i;
+                        tmem_wait_ld();
+                        if (i + 1 < BN / 64) tmem_ld32(taddr + (c + 1) * 32, r[(i + 1) & 1]);
+                        uint4 piece[4];
+                        if (p.epi.residual) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sub[k * 32] = res[i & 1][k];
+                            if (i + 2 < BN / 64) fetch(i + 2);
+                            __syncwarp();
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) piece[g] = own[g ^ own_x];
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t v = r[i & 1][g * 8 + e];
+                                y[e] = nob ? __uint_as_float(v)
+                                           : static_cast<float>(static_cast<int>(v)) * (rs * sw_s[c * 32 + g * 8 + e]);
+                            }
+                            apply_epilogue8(y, bias_s + c * 32 + g * 8, piece[g], p.epi);
+                            __align__(16) __half2 h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                            own[g ^ own_x] = *reinterpret_cast<const uint4 *>(h);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 v = sub[k * 32];
+                            if (sub_col + 32 * i < p.N && sub_row + 8 * k < p.T)
+                                *reinterpret_cast<uint4 *>(p.Y + static_cast<size_t>(sub_row + 8 * k) * p.N + sub_col + 32 * i) = v;
+                        }
+                        __syncwarp();
+                    }
+                }
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
+                for (int c = 0; !kEpi && c < BN / 32; ++c) {
                     const int nc = n0 + c * 32;
                     uint32_t r[32];
                     tmem_ld32(taddr + c * 32, r);
                     tmem_wait_ld();
                     uint4 out[4];
-                    uint4 res_now[4], bia_now[4];
-                    if (kEpi) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) res_now[g] = res[g], bia_now[g] = bia[g];
-                        if (c + 1 < BN / 32) fetch(c + 1);
-                    }
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = g * 8 + e;
-                            y[e] = nob ? __uint_as_float(r[i])
-                                       : static_cast<float>(static_cast<int>(r[i])) * (rs * sw_s[c * 32 + i]);
-                        }
-                        if (kEpi) apply_epilogue8(y, bia_now[g], res_now[g], p.epi.act);
                         __half2 h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = __floats2half2_rn(y[2 * e], y[2 * e + 1]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int i0 = g * 8 + 2 * e, i1 = i0 + 1;
+                            float y0, y1;
+                            if (nob) {
+                                y0 = __uint_as_float(r[i0]);
+                                y1 = __uint_as_float(r[i1]);
+                            } else {
+                                y0 = static_cast<float>(static_cast<int>(r[i0])) * (rs * sw_s[c * 32 + i0]);
+                                y1 = static_cast<float>(static_cast<int>(r[i1])) * (rs * sw_s[c * 32 + i1]);
+                            }
+                            h[e] = __floats2half2_rn(y0, y1);
+                        }
                         out[g] = *reinterpret_cast<uint4 *>(h);
                     }
                     uint8_t *blk = stage_s + (chunk_seq & 1) * EPI_STAGE_BYTES;
@@ -535,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_acc_empty + 8u * buf);
         }
-        if (!kS32 && lane == 0) bulk_wait_group_all();
+        if (!kS32 && !kEpi && lane == 0) bulk_wait_group_all();
         __syncwarp();
     }
 

@@ -140,7 +140,7 @@ i8r_status set_int4_small_attributes() {
 template <int D, int NT>
 cudaError_t set_decode_attention_attribute() {
     return cudaFuncSetAttribute(attn::attention_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                NT == 1 ? 112 * 1024 : 226 * 1024);
+                                static_cast<int>(attn::DEC_SMEM));
 }
 
 i8r_status set_attention_attributes() {
@@ -176,7 +176,7 @@ i8r_status device_setup(const DeviceInfo **out) {
                                           static_cast<int>(prefill2::SMEM_BYTES)));
             I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<false, true>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(prefill2::SMEM_BYTES)));
+                                          static_cast<int>(prefill2::SMEM_BYTES_FUSED)));
             I8R_CUDA(cudaFuncSetAttribute(prefill2::gemm_prefill_pair_kernel<true, false>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(prefill2::SMEM_BYTES)));
@@ -593,16 +593,15 @@ i8r_status launch_prefill(const DeviceInfo *dev, const int8_t *Xq, const __half 
     const int clusters = p.num_tiles < dev->pair_clusters ? p.num_tiles : dev->pair_clusters;
     record_before(s);
     cudaError_t e;
-    auto launch = [&](auto kernel) {
-        return launch_dependent(kernel, dim3(2 * clusters), dim3(prefill2::THREADS), prefill2::SMEM_BYTES, s, 2, map_xq,
-                                map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y, p);
+    auto launch = [&](auto kernel, int threads, size_t smem) {
+        return launch_dependent(kernel, dim3(2 * clusters), dim3(threads), smem, s, 2, map_xq, map_wq, map_xo, map_w16, map_w16x4, map_w16o, map_y, p);
     };
     if (!Y)
-        e = launch(prefill2::gemm_prefill_pair_kernel<true, false>);
+        e = launch(prefill2::gemm_prefill_pair_kernel<true, false>, prefill2::THREADS, prefill2::SMEM_BYTES);
     else if (epi.any())
-        e = launch(prefill2::gemm_prefill_pair_kernel<false, true>);
+        e = launch(prefill2::gemm_prefill_pair_kernel<false, true>, prefill2::THREADS_EPI, prefill2::SMEM_BYTES_FUSED);
     else
-        e = launch(prefill2::gemm_prefill_pair_kernel<false, false>);
+        e = launch(prefill2::gemm_prefill_pair_kernel<false, false>, prefill2::THREADS, prefill2::SMEM_BYTES);
     if (e != cudaSuccess) {
         tl_last_cuda_error = static_cast<int>(e);
         return I8R_ECUDA;
@@ -757,15 +756,6 @@ struct DecodeTiles {
     bool wide() const { return tile > 8; }         // two 8-query MMA columns
 };
 
-// Ring stages of the decode attention's warps: what shared memory leaves, two
-// CTAs an SM for up to 8 queries and one for 16, from 2 to 4.
-int decode_attention_stages(const DecodeTiles &q, int D) {
-    const size_t budget = q.wide() ? 226 * 1024 : 112 * 1024;
-    int stages = 4;
-    while (stages > 2 && attn::decode_smem(q.tile, D, stages) > budget) --stages;
-    return stages;
-}
-
 kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const float *sV, int num_blocks, int H, int D,
                      const int32_t *block_table, int max_blocks) {
     kv::Cache c{};
@@ -782,18 +772,18 @@ kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const 
 }
 
 template <int D>
-i8r_status launch_decode_attention(const DeviceInfo *dev, attn::DecodeParams p, const DecodeTiles &q, cudaStream_t s) {
-    p.stages = decode_attention_stages(q, D);
-    const size_t smem = attn::decode_smem(q.tile, D, p.stages);
-    const int ctas = std::min((q.wide() ? 1 : 2) * dev->sms, attn::DEC_MAX_CTAS);
+i8r_status launch_decode_attention(const DeviceInfo *dev, const attn::DecodeParams &p, const DecodeTiles &q, cudaStream_t s) {
+    const int warps = attn::decode_warps(q.tile, D);
+    const size_t smem = attn::decode_smem(q.tile, D, warps);
+    const int ctas = std::min(dev->sms, attn::DEC_MAX_CTAS);
     if (q.wide())
-        attn::attention_decode_kernel<D, 2><<<ctas, attn::DEC_THREADS, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 2><<<ctas, 32 * warps, smem, s>>>(p);
     else
-        attn::attention_decode_kernel<D, 1><<<ctas, attn::DEC_THREADS, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 1><<<ctas, 32 * warps, smem, s>>>(p);
     I8R_LAUNCHED();
     if (ctas > 1) {
         const cudaError_t e = launch_dependent(attn::attention_combine_kernel<D>, dim3(ctas - 1, q.tile), dim3(D), 0, s, 1,
-                                               p, ctas);
+                                               p, ctas, warps);
         if (e != cudaSuccess) {
             tl_last_cuda_error = static_cast<int>(e);
             return I8R_ECUDA;
@@ -1346,7 +1336,8 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     p.G = q.G;
     p.GT = q.GT;
     p.tile = q.tile;
-    p.scale_log2 = scale * 1.44269504088896340736f;      // log2(e)
+    p.scale_log2 = std::fabs(scale) * 1.44269504088896340736f;      // log2(e)
+    p.negate = scale < 0.0f ? 0x80008000u : 0u;
     p.part = static_cast<float *>(workspace);
     return D == 128 ? launch_decode_attention<128>(dev, p, q, stream) : launch_decode_attention<64>(dev, p, q, stream);
 }
