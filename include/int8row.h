@@ -317,7 +317,7 @@ void int4_debug_set_product_path(int mode);
  *     code * s / 127; s = 0 gives codes 0;
  *   - block_table [B, max_blocks] int32: the number in [0, num_blocks) of the
  *     block that holds block i of sequence b; entries past a sequence's length
- *     are not read;
+ *     have no effect;
  *   - when rows are added to a partly filled block, its scale becomes
  *     max(old scale, absmax of the new rows), and if that is larger than the
  *     old one the codes already there become rhaz(code * fl32(old / new)).  A

@@ -14,10 +14,9 @@
 // shared memory, and the few items that cross CTAs by attention_combine_kernel
 // from at most two pieces a CTA, always in the same order.
 //
-// The codes travel by cp.async into slots that only the copying lane reads (they
-// are its registers to come: no barrier, no bank conflict), eight sub-tiles of 16
-// tokens of K or V a warp, each asked for again as soon as it has been read, so a
-// whole block per warp is always on its way.  A lane's bytes are its own mma.sync
+// The codes travel by cp.async into the warp's own slots, four sub-tiles of 16
+// tokens: as K's are read, V's are asked for, and as V's are read, the next
+// block's K.  With 12 warps that is 48 to 96 KB on the way to every SM.  A lane's bytes are its own mma.sync
 // fragments: m16n8k16 with tokens (then V's columns) as the 16 rows and queries as
 // the 8 columns, which suits one to eight queries per head; at one MMA in ten
 // cycles the legacy tensor path is nowhere near a limit.
@@ -56,12 +55,16 @@ struct DecodeParams {
     float *part;                         // [2 * CTAs][tile][D + 2]
 };
 
-// Bytes of one warp's slots (a block of K and of V).
-__host__ __device__ constexpr int ring_bytes(int D) { return 2 * kv::BLOCK * D; }
 // Floats of one piece: maximum, sum and D values per query.
 __host__ __device__ constexpr int piece_floats(int tile, int D) { return tile * (D + 2); }
+// Bytes of one warp's slots: four sub-tiles, K's and V's in turn; in the end its
+// last piece, which may be a little larger.
+__host__ __device__ constexpr int ring_bytes(int tile, int D) {
+    const int piece = (piece_floats(tile, D) * 4 + 15) / 16 * 16;
+    return piece > kv::BLOCK * D ? piece : kv::BLOCK * D;
+}
 __host__ __device__ constexpr size_t decode_smem(int tile, int D, int warps) {
-    return static_cast<size_t>(warps) * (ring_bytes(D) + piece_floats(tile, D) * 4);
+    return static_cast<size_t>(warps) * (ring_bytes(tile, D) + piece_floats(tile, D) * 4);
 }
 // Warps per CTA, one CTA an SM: registers allow 12 (8 with two MMA columns of
 // queries), shared memory fewer for wide tiles.
@@ -73,9 +76,6 @@ __host__ inline int decode_warps(int tile, int D) {
     return warps;
 }
 
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -249,11 +249,26 @@ struct Place {
     }
 };
 
-// The block of a place; a bad number (reported) reads block 0, which is always there.
-__device__ __forceinline__ int page_at(const DecodeParams &p, const Place &w) {
-    const int page = kv::block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, w.b, w.step / SUBS);
-    return page < 0 ? 0 : page;
-}
+// A window of 32 of a sequence's block numbers, one a lane: the table is read once
+// per 32 blocks (and serves all heads of a shorter sequence), not in front of every
+// block's codes.
+struct Window {
+    int b = -1, first = 0, mine = 0;
+    // the block of a place; a bad number (reported) reads block 0, which is always there
+    __device__ __forceinline__ int page(const DecodeParams &p, const Place &w) {
+        const int i = w.step / SUBS;
+        if (w.b != b || i < first || i >= first + 32) {
+            b = w.b;
+            first = i & ~31;
+            const int at = first + (threadIdx.x & 31);
+            mine = at < p.c.max_blocks ? p.c.table[static_cast<size_t>(b) * p.c.max_blocks + at] : -1;
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, mine, i - first);
+        if (page >= 0 && page < p.c.num_blocks) return page;
+        report_status(I8R_DEV_BAD_INDEX);
+        return 0;
+    }
+};
 
 // The address of a place's block of K or V for its head.
 template <int D>
@@ -261,9 +276,9 @@ __device__ __forceinline__ const int8_t *block_codes(const DecodeParams &p, cons
     return (kv ? p.c.codes[1] : p.c.codes[0]) + (static_cast<size_t>(page) * p.c.H + w.h) * (kv::BLOCK * D);
 }
 
-// Sub-tile j (16 tokens) of K and of V: this lane's bytes of it, in the order in
-// which they are read back.  K: rows (tokens) g and g + 8, 16 bytes at 16t of each
-// 64; V: rows 2t, 2t+1, 2t+8, 2t+9, the D/8 bytes at g*D/8.
+// Sub-tile j (16 tokens) of K: this lane's own bytes of it, in the order in which
+// it reads them back: rows (tokens) g and g + 8, 16 bytes at 16t of each 64.  Four
+// neighbouring lanes cover 64 bytes of a row.
 template <int D>
 __device__ __forceinline__ void issue_k(const int8_t *K, int j, uint32_t ring) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -274,18 +289,35 @@ __device__ __forceinline__ void issue_k(const int8_t *K, int j, uint32_t ring) {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c, dst += 512) cp_async_16(dst, src + 8 * r * D + 64 * c, 16u);
 }
+
+// Sub-tile j of V: a lane reads rows 2t, 2t+1, 2t+8, 2t+9, the D/8 bytes at g*D/8 of
+// each, which for neighbouring lanes lie in different rows.  Copied that way, every
+// 32 bytes were a request of their own (three times the L1's requests and half as
+// many sectors again: 4.6 TB/s without any arithmetic, for 6.3 in whole rows); so
+// the lanes copy whole rows for one another.  Row r's bytes are at v_row(r), its
+// 16-byte pieces swapped by v_swap(r), which keeps both the copies' and the
+// reads' eight lanes on different banks.
+template <int D>
+__device__ __forceinline__ int v_row(int r) {
+    // D = 128: the four rows of one MMA register (t = 0..3) side by side; D = 64: even
+    // and odd t in the two halves of 128 bytes
+    const int t = (r >> 1) & 3, k = (r & 1) + 2 * (r >> 3);
+    return (4 * k + t) * D;
+}
+template <int D>
+__device__ __forceinline__ int v_swap(int r) {
+    const int t = (r >> 1) & 3;
+    return D == 128 ? 2 * t : 2 * (t >> 1);
+}
 template <int D>
 __device__ __forceinline__ void issue_v(const int8_t *V, int j, uint32_t ring) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int8_t *src = V + (STEP * j + 2 * t) * D + g * (D / 8);
-    const uint32_t dst = ring + (SUBS + j) * (STEP * D) + lane * (D / 8);
+    constexpr int PIECES = D / 16, ROWS = 32 / PIECES;          // 16-byte pieces of a row, rows per instruction
+    const int lane = threadIdx.x & 31, piece = lane % PIECES;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int8_t *s = src + ((k & 1) + 8 * (k >> 1)) * D;
-        if (D == 128)
-            cp_async_16(dst + k * 512, s, 16u);
-        else
-            cp_async_8(dst + k * 256, s);
+    for (int i = 0; i < STEP / ROWS; ++i) {
+        const int r = i * ROWS + lane / PIECES;
+        cp_async_16(ring + j * (STEP * D) + v_row<D>(r) + ((piece ^ v_swap<D>(r)) << 4),
+                    V + (STEP * j + r) * D + 16 * piece, 16u);
     }
 }
 
@@ -454,16 +486,18 @@ struct State {
 
     // Sub-tile j's values: rows are columns d of V, two per lane and MMA; k is the token.
     __device__ __forceinline__ void values(const uint8_t *ring, int j, const uint32_t (&pf)[NT][2]) {
-        const uint8_t *mine = ring + (SUBS + j) * (STEP * D) + (threadIdx.x & 31) * (D / 8);
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+            const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+            const uint8_t *mine = ring + j * (STEP * D) + v_row<D>(r);
             if (D == 128) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(mine + 512 * k);
-                v[k][0] = r.x, v[k][1] = r.y, v[k][D / 32 - 2] = r.z, v[k][D / 32 - 1] = r.w;
+                const uint4 w = *reinterpret_cast<const uint4 *>(mine + ((g ^ v_swap<D>(r)) << 4));
+                v[k][0] = w.x, v[k][1] = w.y, v[k][D / 32 - 2] = w.z, v[k][D / 32 - 1] = w.w;
             } else {
-                const uint2 r = *reinterpret_cast<const uint2 *>(mine + 256 * k);
-                v[k][0] = r.x, v[k][1] = r.y;
+                const uint2 w = *reinterpret_cast<const uint2 *>(mine + (((g >> 1) ^ v_swap<D>(r)) << 4) + 8 * (g & 1));
+                v[k][0] = w.x, v[k][1] = w.y;
             }
         }
 #pragma unroll
@@ -531,10 +565,11 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
     __shared__ Piece pieces[2 * DEC_WARPS_1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta_warps = blockDim.x >> 5;
-    uint8_t *ring = smem + warp * ring_bytes(D);
+    const int warp_ring = ring_bytes(p.tile, D);
+    uint8_t *ring = smem + warp * warp_ring;
     const uint32_t ring_u = smem_u32(ring);
     // a warp's first piece is written while its slots are still in use, its last one into them
-    float *firsts = reinterpret_cast<float *>(smem + cta_warps * ring_bytes(D));
+    float *firsts = reinterpret_cast<float *>(smem + cta_warps * warp_ring);
     if (lane < 2) pieces[2 * warp + lane].b = -1;
     __syncwarp();
     griddep_launch_dependents();         // combine_kernel may find its items meanwhile (it fits in beside no CTA of this grid)
@@ -547,21 +582,18 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
         Place w;
         w.at(p, order, u0);
         w.cut(u1 - u0);
-        int page = page_at(p, w);
+        Window window;
+        int page = window.page(p, w);
         {
-            const int8_t *K = block_codes<D>(p, w, page, 0), *V = block_codes<D>(p, w, page, 1);
+            const int8_t *K = block_codes<D>(p, w, page, 0);
             const int j0 = w.step & (SUBS - 1), j1 = j0 + w.count;
 #pragma unroll
             for (int j = 0; j < SUBS; ++j) {
                 if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
                 if (j & 1) cp_async_commit();
             }
-#pragma unroll
-            for (int j = 0; j < SUBS; ++j) {
-                if (j >= j0 && j < j1) issue_v<D>(V, j, ring_u);
-                if (j & 1) cp_async_commit();
-            }
         }
+        const int8_t *V = block_codes<D>(p, w, page, 1);
         size_t at = static_cast<size_t>(page) * p.c.H + w.h;
         float sk = __ldg(p.c.scale[0] + at), sv = __ldg(p.c.scale[1] + at);
         State<D, NT> st;
@@ -571,48 +603,53 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
         if (done < u1) {
             ahead.next(p, order);
             ahead.cut(u1 - done);
-            page = page_at(p, ahead);
+            page = window.page(p, ahead);
         }
         bool starts = w.step == 0, first = true;
         while (true) {
             // the block after this one: its scales now, its codes as the slots come free
             const bool more = done < u1;
-            const int8_t *K = nullptr, *V = nullptr;
+            const int8_t *K = nullptr, *V_next = nullptr;
             float sk_next = 0.0f, sv_next = 0.0f;
             int j0 = SUBS, j1 = 0;
             if (more) {
                 K = block_codes<D>(p, ahead, page, 0);
-                V = block_codes<D>(p, ahead, page, 1);
+                V_next = block_codes<D>(p, ahead, page, 1);
                 at = static_cast<size_t>(page) * p.c.H + ahead.h;
                 sk_next = __ldg(p.c.scale[0] + at);
                 sv_next = __ldg(p.c.scale[1] + at);
                 j0 = ahead.step & (SUBS - 1);
                 j1 = j0 + ahead.count;
             }
+            const int i0 = w.step & (SUBS - 1), i1 = i0 + w.count;
             float x[SUBS / 2][2][NT][4];
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
-                cp_async_wait<SUBS - 1>();
+                cp_async_wait<1>();
                 st.scores(ring, j, x[j / 2]);
-                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
-                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
+                __syncwarp();                // read by all: the lanes copy V for one another
+                if (j >= i0 && j < i1) issue_v<D>(V, j, ring_u);
+                if (j + 1 >= i0 && j + 1 < i1) issue_v<D>(V, j + 1, ring_u);
                 cp_async_commit();
             }
-            const int lo = (w.step & (SUBS - 1)) * STEP;
+            const int lo = i0 * STEP;
             const int hi = min(lo + w.count * STEP, w.len - w.step / SUBS * kv::BLOCK);
             uint32_t pf[SUBS][NT][2];
             st.weigh(p, x, sk, sv, lo, hi, pf);
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
-                cp_async_wait<SUBS - 1>();
+                cp_async_wait<1>();
+                __syncwarp();
                 if (sv != 0.0f) {
                     st.values(ring, j, pf[j]);
                     st.values(ring, j + 1, pf[j + 1]);
                 }
-                if (j >= j0 && j < j1) issue_v<D>(V, j, ring_u);
-                if (j + 1 >= j0 && j + 1 < j1) issue_v<D>(V, j + 1, ring_u);
+                __syncwarp();
+                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
+                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
                 cp_async_commit();
             }
+            V = V_next;
             const bool ends = w.step + w.count == w.steps;
             if (ends || !more) {
                 const bool whole = starts && ends;
@@ -633,7 +670,7 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
             if (done < u1) {
                 ahead.next(p, order);
                 ahead.cut(u1 - done);
-                page = page_at(p, ahead);
+                page = window.page(p, ahead);
             }
         }
     }
@@ -644,7 +681,7 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
     // where the CTA's range does, else in slot 1.
     const long long U0 = order.begin(blockIdx.x * cta_warps);
     auto piece_of = [&](int k) {
-        return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * ring_bytes(D))
+        return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)
                        : firsts + (k >> 1) * piece_floats(p.tile, D);
     };
     for (int i = 0; i < 2 * cta_warps;) {
