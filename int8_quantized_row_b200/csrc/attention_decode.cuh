@@ -52,7 +52,8 @@ struct DecodeParams {
     int B, G, GT, tile;                  // queries per kv head, tiles of `tile` queries per kv head
     float scale_log2;                    // |scale| * log2(e)
     uint32_t negate;                     // sign bits that the queries are flipped by: scale < 0
-    float *part;                         // [2 * CTAs][tile][D + 2]
+    float *part;                         // [2 * CTAs][tile][D + 2]: pieces that cross CTAs
+    float *firsts;                       // [warps of the grid][tile][D + 2]: warps' first pieces (wide tiles)
 };
 
 // Floats of one piece: maximum, sum and D values per query.
@@ -63,20 +64,26 @@ __host__ __device__ constexpr int ring_bytes(int tile, int D) {
     const int piece = (piece_floats(tile, D) * 4 + 15) / 16 * 16;
     return piece > kv::BLOCK * D ? piece : kv::BLOCK * D;
 }
+// Bytes of one warp's queries, in the order of their MMA fragments.
+__host__ __device__ constexpr int query_bytes(int tile, int D) { return D / 16 * (tile > 8 ? 2 : 1) * 256; }
 __host__ __device__ constexpr size_t decode_smem(int tile, int D, int warps) {
-    return static_cast<size_t>(warps) * (ring_bytes(tile, D) + piece_floats(tile, D) * 4);
+    return static_cast<size_t>(warps) *
+           (ring_bytes(tile, D) + query_bytes(tile, D) + (tile > 8 ? 0 : piece_floats(tile, D) * 4));
 }
-// Warps per CTA, one CTA an SM: registers allow 12 (8 with two MMA columns of
-// queries), shared memory fewer for wide tiles.
-constexpr int DEC_WARPS_1 = 12, DEC_WARPS_2 = 8;
+// Warps per CTA, one CTA an SM: 168 registers a lane.  (With two MMA columns of
+// queries that takes the queries' fragments out of registers, read from shared
+// memory for every 32 tokens; 8 warps of 255 registers were slower.)
+constexpr int DEC_WARPS = 12;
 constexpr size_t DEC_SMEM = 226 * 1024;
-__host__ inline int decode_warps(int tile, int D) {
-    int warps = tile > 8 ? DEC_WARPS_2 : DEC_WARPS_1;
-    while (decode_smem(tile, D, warps) > DEC_SMEM) --warps;
-    return warps;
-}
+static_assert(decode_smem(8, 128, DEC_WARPS) <= DEC_SMEM && decode_smem(16, 128, DEC_WARPS) <= DEC_SMEM &&
+              decode_smem(8, 64, DEC_WARPS) <= DEC_SMEM && decode_smem(16, 64, DEC_WARPS) <= DEC_SMEM,
+              "the widest tiles fit");
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// 8-byte asynchronous copy global -> shared; zeros instead with src_bytes = 0.
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -136,9 +143,12 @@ struct Steps {
     long long before;                    // steps of the sequences before this lane's four
     long long total;
     int warps;                           // of the grid
+    long long share;                     // units (blocks or steps) of a warp, and what is left over
+    int rest;
     bool coarse;
 
-    __device__ __forceinline__ int item(int n) const {
+    __device__ __forceinline__ int item(int n) const { return item(n, coarse); }
+    __device__ __forceinline__ static int item(int n, bool coarse) {
         return coarse ? (n + kv::BLOCK - 1) / kv::BLOCK * SUBS : (n + STEP - 1) / STEP;
     }
     __device__ __forceinline__ static void lengths(const DecodeParams &p, int b0, int (&n)[4]) {
@@ -176,10 +186,14 @@ struct Steps {
             coarse = false;
             sum(p);
         }
+        const long long units = coarse ? total / SUBS : total;
+        share = units / warps;
+        rest = static_cast<int>(units - share * warps);
     }
-    // The first step of warp w's range.
+    // The first step of warp w's range: floor(units * w / warps) units.
     __device__ __forceinline__ long long begin(int w) const {
-        return coarse ? total / SUBS * w / warps * SUBS : total * w / warps;
+        const long long u = share * w + static_cast<unsigned>(rest * w) / static_cast<unsigned>(warps);
+        return coarse ? u * SUBS : u;
     }
     // The sequence (and its length), item and step of step u < total.
     __device__ __forceinline__ void find(const DecodeParams &p, long long u, int *b, int *n, int *hg, int *step) const {
@@ -220,20 +234,21 @@ struct Steps {
 // key/value head h, query tile gt), all in one block.
 struct Place {
     int b, h, gt, step, count, steps, len;
+    bool coarse;
     __device__ __forceinline__ void at(const DecodeParams &p, const Steps &order, long long u) {
         int hg;
         order.find(p, u, &b, &len, &hg, &step);
         steps = order.item(len);
         h = hg / p.GT;
         gt = hg % p.GT;
+        coarse = order.coarse;
     }
     // the rest of the block that `step` lies in, of the item, and of the range
-    __device__ __forceinline__ void cut(long long left) {
-        count = min(SUBS - (step & (SUBS - 1)), steps - step);
-        if (left < count) count = static_cast<int>(left);
+    __device__ __forceinline__ void cut(int left) {
+        count = min(left, min(SUBS - (step & (SUBS - 1)), steps - step));
     }
     // the step after these; only called while the range has one
-    __device__ __forceinline__ void next(const DecodeParams &p, const Steps &order) {
+    __device__ __forceinline__ void next(const DecodeParams &p) {
         step += count;
         if (step < steps) return;
         step = 0;
@@ -245,7 +260,7 @@ struct Place {
             if (++b >= p.B) return;
             len = length_of(p, b);
         } while (len == 0);
-        steps = order.item(len);
+        steps = Steps::item(len, coarse);
     }
 };
 
@@ -254,8 +269,9 @@ struct Place {
 // block's codes.
 struct Window {
     int b = -1, first = 0, mine = 0;
-    // the block of a place; a bad number (reported) reads block 0, which is always there
-    __device__ __forceinline__ int page(const DecodeParams &p, const Place &w) {
+    // where a place's block and head lie, in blocks of one head (the host checks that
+    // 32 bits hold them); a bad block number (reported) reads block 0, which is always there
+    __device__ __forceinline__ uint32_t slot(const DecodeParams &p, const Place &w) {
         const int i = w.step / SUBS;
         if (w.b != b || i < first || i >= first + 32) {
             b = w.b;
@@ -263,17 +279,18 @@ struct Window {
             const int at = first + (threadIdx.x & 31);
             mine = at < p.c.max_blocks ? p.c.table[static_cast<size_t>(b) * p.c.max_blocks + at] : -1;
         }
-        const int page = __shfl_sync(0xFFFFFFFFu, mine, i - first);
-        if (page >= 0 && page < p.c.num_blocks) return page;
-        report_status(I8R_DEV_BAD_INDEX);
-        return 0;
+        int page = __shfl_sync(0xFFFFFFFFu, mine, i - first);
+        if (page < 0 || page >= p.c.num_blocks) {
+            report_status(I8R_DEV_BAD_INDEX);
+            page = 0;
+        }
+        return static_cast<uint32_t>(page) * p.c.H + w.h;
     }
 };
 
-// The address of a place's block of K or V for its head.
 template <int D>
-__device__ __forceinline__ const int8_t *block_codes(const DecodeParams &p, const Place &w, int page, int kv) {
-    return (kv ? p.c.codes[1] : p.c.codes[0]) + (static_cast<size_t>(page) * p.c.H + w.h) * (kv::BLOCK * D);
+__device__ __forceinline__ const int8_t *block_codes(const int8_t *codes, uint32_t slot) {
+    return codes + static_cast<size_t>(slot) * (kv::BLOCK * D);
 }
 
 // Sub-tile j (16 tokens) of K: this lane's own bytes of it, in the order in which
@@ -321,6 +338,24 @@ __device__ __forceinline__ void issue_v(const int8_t *V, int j, uint32_t ring) {
     }
 }
 
+// The queries of an item, this lane's own fragments: for each 16 values of D and 8
+// queries, values 16t + 64 (k/4) + 4 (k%4) .. + 3 of query g (zeros past the last one).
+template <int D, int NT>
+__device__ __forceinline__ void issue_q(const DecodeParams &p, const Place &w, uint32_t queries) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int q0 = w.gt * p.tile;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int qi = 8 * n + g;
+        const bool have = q0 + qi < p.G && qi < p.tile;
+        const __half *src = p.Q + static_cast<size_t>(w.b) * p.ldq;
+        if (have) src += static_cast<size_t>(w.h * p.G + q0 + qi) * D + 16 * t;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            cp_async_8(queries + (k * NT + n) * 256 + lane * 8, have ? src + 64 * (k >> 2) + 4 * (k & 3) : src, have ? 8u : 0u);
+    }
+}
+
 // One piece of an item in memory: per query its maximum (log2 units), its sum
 // and its D unnormalised values.
 template <int D>
@@ -332,37 +367,12 @@ struct State {
     float m[NT][2], l[NT][2];            // of this lane's queries 2t, 2t + 1: the same in all its g
     float vs;                            // the scale acc is in (sV/127 of the last block with any)
     float start[NT][2];                  // -1152 sum(Q): what a score starts at
-    uint32_t q[D / 16][NT][2];
+    uint2 q[NT == 1 ? D / 16 : 1];       // the queries' fragments (NT = 1)
 
-    // a new item: its queries (zero past the last one), nothing summed yet
-    __device__ __forceinline__ void begin(const DecodeParams &p, const Place &w) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const int h = w.h, q0 = w.gt * p.tile;
+    // a new item: nothing summed yet
+    __device__ __forceinline__ void begin() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int qi = q0 + 8 * n + g;
-            const bool have = qi < p.G && 8 * n + g < p.tile;
-            const __half *src = p.Q + static_cast<size_t>(w.b) * p.ldq + static_cast<size_t>(h * p.G + qi) * D + 16 * t;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint2 v = have ? __ldg(reinterpret_cast<const uint2 *>(src + 64 * (k >> 2) + 4 * (k & 3)))
-                                     : make_uint2(0u, 0u);
-                q[k][n][0] = v.x;
-                q[k][n][1] = v.y;
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    q[k][n][r] ^= p.negate;
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&q[k][n][r]));
-                    sum += f.x + f.y;
-                }
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) start[n][e] = -kCodeBias * __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * e);
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.0f;
         }
@@ -375,12 +385,40 @@ struct State {
                 for (int e = 0; e < 4; ++e) acc[k][n][e] = 0.0f;
     }
 
+    // its queries, once they have come
+    __device__ __forceinline__ void take_queries(const DecodeParams &p, uint8_t *queries) {
+        const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint2 *at = reinterpret_cast<uint2 *>(queries + (k * NT + n) * 256) + lane;
+                uint2 v = *at;
+                v.x ^= p.negate;
+                v.y ^= p.negate;
+                if (NT == 1)
+                    q[k] = v;
+                else if (p.negate)
+                    *at = v;
+                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
+                const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
+                sum += (a.x + a.y) + (b.x + b.y);
+            }
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) start[n][e] = -kCodeBias * __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * e);
+        }
+    }
+
     // Scores of sub-tiles j and j + 1: rows are tokens g and g+8, a lane's four
     // codes of a word are the MMA's columns 2t, 2t+1, 2t+8, 2t+9 (so are the
-    // queries').  Four chains of MMAs go side by side (two sub-tiles, two halves
-    // of each sum): a chain alone waits for each MMA's result.
-    __device__ __forceinline__ void scores(const uint8_t *ring, int j, float (&x)[2][NT][4]) const {
+    // queries').  Four chains of MMAs go side by side (two sub-tiles, and two halves
+    // of each sum or two columns of queries): a chain alone waits for each MMA's result.
+    __device__ __forceinline__ void scores(const uint8_t *ring, const uint8_t *queries, int j, float (&x)[2][NT][4]) const {
         float y[2][NT][4];
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -395,14 +433,19 @@ struct State {
             uint32_t a[2][4], b[2][4];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const uint8_t *mine = ring + (j + s) * (STEP * D) + (threadIdx.x & 31) * 16;
+                const uint8_t *mine = ring + (j + s) * (STEP * D) + lane * 16;
                 const uint4 r0 = *reinterpret_cast<const uint4 *>(mine + 512 * c);
                 const uint4 r1 = *reinterpret_cast<const uint4 *>(mine + 512 * (D / 64 + c));
                 a[s][0] = r0.x, a[s][1] = r0.y, a[s][2] = r0.z, a[s][3] = r0.w;
                 b[s][0] = r1.x, b[s][1] = r1.y, b[s][2] = r1.z, b[s][3] = r1.w;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
+                uint2 f[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    f[n] = NT == 1 ? q[4 * c + k]
+                                   : reinterpret_cast<const uint2 *>(queries + ((4 * c + k) * NT + n) * 256)[lane];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t u = a[s][k] ^ 0x80808080u, v = b[s][k] ^ 0x80808080u;
@@ -410,15 +453,16 @@ struct State {
                     const uint32_t a1 = biased_codes<0x4140>(v), a3 = biased_codes<0x4342>(v);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816((k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, q[4 * c + k][n][0], q[4 * c + k][n][1]);
+                        mma16816(NT == 1 && (k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, f[n].x, f[n].y);
                 }
+            }
         }
+        if (NT == 1) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[s][n][e] += y[s][n][e];
+                for (int e = 0; e < 4; ++e) x[s][0][e] += y[s][0][e];
+        }
     }
 
     // The block's scores become weights (in `pf`, as the second product's
@@ -556,36 +600,48 @@ struct State {
 struct Piece {
     int b, h, gt;                        // b < 0: none
     bool starts, ends;                   // the piece holds the item's first / last step
+    bool front;                          // it begins where the CTA's range begins
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
+__global__ void __launch_bounds__(32 * DEC_WARPS, 1)
     attention_decode_kernel(const __grid_constant__ DecodeParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Piece pieces[2 * DEC_WARPS_1];
+    __shared__ Piece pieces[2 * DEC_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cta_warps = blockDim.x >> 5;
+    constexpr int cta_warps = DEC_WARPS;
     const int warp_ring = ring_bytes(p.tile, D);
     uint8_t *ring = smem + warp * warp_ring;
     const uint32_t ring_u = smem_u32(ring);
-    // a warp's first piece is written while its slots are still in use, its last one into them
-    float *firsts = reinterpret_cast<float *>(smem + cta_warps * warp_ring);
+    uint8_t *queries = smem + cta_warps * warp_ring + warp * query_bytes(p.tile, D);
+    const uint32_t queries_u = smem_u32(queries);
+    // a warp's first piece is written while its slots are still in use (a wide tile's
+    // would take a third of shared memory: it goes to the workspace), its last one into them
+    float *firsts = NT == 1 ? reinterpret_cast<float *>(smem + cta_warps * (warp_ring + query_bytes(p.tile, D)))
+                            : p.firsts + static_cast<size_t>(blockIdx.x) * cta_warps * piece_floats(p.tile, D);
     if (lane < 2) pieces[2 * warp + lane].b = -1;
     __syncwarp();
     griddep_launch_dependents();         // combine_kernel may find its items meanwhile (it fits in beside no CTA of this grid)
 
-    Steps order;
-    order.load(p, gridDim.x * cta_warps);
-    const int me = blockIdx.x * cta_warps + warp;
-    const long long u0 = order.begin(me), u1 = order.begin(me + 1);
+    Place w, ahead;
+    long long u0, u1;
+    bool front;
+    {
+        Steps order;
+        order.load(p, gridDim.x * cta_warps);
+        u0 = order.begin(blockIdx.x * cta_warps + warp);
+        u1 = order.begin(blockIdx.x * cta_warps + warp + 1);
+        front = u0 == order.begin(blockIdx.x * cta_warps);
+        if (u0 < u1) w.at(p, order, u0);
+    }
     if (u0 < u1) {
-        Place w;
-        w.at(p, order, u0);
-        w.cut(u1 - u0);
+        int left = static_cast<int>(min(u1 - u0, 0x7FFFFFFFll));      // steps of the range from w on
+        w.cut(left);
         Window window;
-        int page = window.page(p, w);
+        uint32_t slot = window.slot(p, w), slot_next = 0;
+        issue_q<D, NT>(p, w, queries_u);
         {
-            const int8_t *K = block_codes<D>(p, w, page, 0);
+            const int8_t *K = block_codes<D>(p.c.codes[0], slot);
             const int j0 = w.step & (SUBS - 1), j1 = j0 + w.count;
 #pragma unroll
             for (int j = 0; j < SUBS; ++j) {
@@ -593,41 +649,34 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
                 if (j & 1) cp_async_commit();
             }
         }
-        const int8_t *V = block_codes<D>(p, w, page, 1);
-        size_t at = static_cast<size_t>(page) * p.c.H + w.h;
-        float sk = __ldg(p.c.scale[0] + at), sv = __ldg(p.c.scale[1] + at);
+        float sk = __ldg(p.c.scale[0] + slot), sv = __ldg(p.c.scale[1] + slot);
         State<D, NT> st;
-        st.begin(p, w);
-        long long done = u0 + w.count;               // steps of the range up to the end of w
-        Place ahead = w;
-        if (done < u1) {
-            ahead.next(p, order);
-            ahead.cut(u1 - done);
-            page = window.page(p, ahead);
+        st.begin();
+        left -= w.count;
+        ahead = w;
+        if (left > 0) {
+            ahead.next(p);
+            ahead.cut(left);
+            slot_next = window.slot(p, ahead);
         }
-        bool starts = w.step == 0, first = true;
+        bool starts = w.step == 0, first = true, fresh = true;
         while (true) {
             // the block after this one: its scales now, its codes as the slots come free
-            const bool more = done < u1;
-            const int8_t *K = nullptr, *V_next = nullptr;
+            const bool more = left > 0, ends = w.step + w.count == w.steps;
             float sk_next = 0.0f, sv_next = 0.0f;
-            int j0 = SUBS, j1 = 0;
             if (more) {
-                K = block_codes<D>(p, ahead, page, 0);
-                V_next = block_codes<D>(p, ahead, page, 1);
-                at = static_cast<size_t>(page) * p.c.H + ahead.h;
-                sk_next = __ldg(p.c.scale[0] + at);
-                sv_next = __ldg(p.c.scale[1] + at);
-                j0 = ahead.step & (SUBS - 1);
-                j1 = j0 + ahead.count;
+                sk_next = __ldg(p.c.scale[0] + slot_next);
+                sv_next = __ldg(p.c.scale[1] + slot_next);
             }
             const int i0 = w.step & (SUBS - 1), i1 = i0 + w.count;
             float x[SUBS / 2][2][NT][4];
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
                 cp_async_wait<1>();
-                st.scores(ring, j, x[j / 2]);
+                if (j == 0 && fresh) st.take_queries(p, queries);
+                st.scores(ring, queries, j, x[j / 2]);
                 __syncwarp();                // read by all: the lanes copy V for one another
+                const int8_t *V = block_codes<D>(p.c.codes[1], slot);
                 if (j >= i0 && j < i1) issue_v<D>(V, j, ring_u);
                 if (j + 1 >= i0 && j + 1 < i1) issue_v<D>(V, j + 1, ring_u);
                 cp_async_commit();
@@ -636,6 +685,7 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
             const int hi = min(lo + w.count * STEP, w.len - w.step / SUBS * kv::BLOCK);
             uint32_t pf[SUBS][NT][2];
             st.weigh(p, x, sk, sv, lo, hi, pf);
+            const int j0 = ahead.step & (SUBS - 1), j1 = more ? j0 + ahead.count : 0;
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
                 cp_async_wait<1>();
@@ -645,32 +695,32 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
                     st.values(ring, j + 1, pf[j + 1]);
                 }
                 __syncwarp();
+                const int8_t *K = block_codes<D>(p.c.codes[0], slot_next);
+                if (j == 0 && ends && more) issue_q<D, NT>(p, ahead, queries_u);
                 if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
                 if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
                 cp_async_commit();
             }
-            V = V_next;
-            const bool ends = w.step + w.count == w.steps;
+            fresh = ends;
             if (ends || !more) {
                 const bool whole = starts && ends;
-                if (!whole) {
-                    if (!first) __syncwarp();        // the range's last steps: every lane has read its slots
-                    if (lane == 0) pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.h, w.gt, starts, ends};
-                }
+                if (!whole && lane == 0)
+                    pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.h, w.gt, starts, ends, first && front};
                 st.end(p, w, whole, first ? firsts + warp * piece_floats(p.tile, D) : reinterpret_cast<float *>(ring));
                 first = false;
                 starts = true;
-                if (more) st.begin(p, ahead);
+                st.begin();
             }
             if (!more) break;
             w = ahead;
+            slot = slot_next;
             sk = sk_next;
             sv = sv_next;
-            done += w.count;
-            if (done < u1) {
-                ahead.next(p, order);
-                ahead.cut(u1 - done);
-                page = window.page(p, ahead);
+            left -= w.count;
+            if (left > 0) {
+                ahead.next(p);
+                ahead.cut(left);
+                slot_next = window.slot(p, ahead);
             }
         }
     }
@@ -679,7 +729,6 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
     // Merge this CTA's pieces, item by item in order; an item that begins or ends
     // in another CTA leaves one piece for combine_kernel, in slot 0 if it begins
     // where the CTA's range does, else in slot 1.
-    const long long U0 = order.begin(blockIdx.x * cta_warps);
     auto piece_of = [&](int k) {
         return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)
                        : firsts + (k >> 1) * piece_floats(p.tile, D);
@@ -697,8 +746,7 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
             last = j;
         }
         const bool whole = a.starts && pieces[last].ends;
-        const int first_warp = blockIdx.x * cta_warps + (i >> 1);
-        const int out_slot = ((i & 1) == 0 && order.begin(first_warp) == U0) ? 0 : 1;
+        const int out_slot = a.front ? 0 : 1;
         float *out = p.part + static_cast<size_t>(2 * blockIdx.x + out_slot) * piece_floats(p.tile, D);
         const int h = a.h, q0 = a.gt * p.tile;
         const int nq = min(p.tile, p.G - q0);
@@ -747,7 +795,8 @@ __global__ void __launch_bounds__(32 * (NT == 1 ? DEC_WARPS_1 : DEC_WARPS_2), 1)
 // value; the pieces are read in order, eight at a time.  Launched as a
 // programmatic dependent: which item it is, is known from the lengths alone.
 template <int D>
-__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas, int cta_warps) {
+__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas) {
+    constexpr int cta_warps = DEC_WARPS;
     const int c = blockIdx.x, q = blockIdx.y, d = threadIdx.x;
     Steps order;
     order.load(p, ctas * cta_warps);

@@ -773,17 +773,17 @@ kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const 
 
 template <int D>
 i8r_status launch_decode_attention(const DeviceInfo *dev, const attn::DecodeParams &p, const DecodeTiles &q, cudaStream_t s) {
-    const int warps = attn::decode_warps(q.tile, D);
-    const size_t smem = attn::decode_smem(q.tile, D, warps);
+    constexpr int threads = 32 * attn::DEC_WARPS;
+    const size_t smem = attn::decode_smem(q.tile, D, attn::DEC_WARPS);
     const int ctas = std::min(dev->sms, attn::DEC_MAX_CTAS);
     if (q.wide())
-        attn::attention_decode_kernel<D, 2><<<ctas, 32 * warps, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 2><<<ctas, threads, smem, s>>>(p);
     else
-        attn::attention_decode_kernel<D, 1><<<ctas, 32 * warps, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 1><<<ctas, threads, smem, s>>>(p);
     I8R_LAUNCHED();
     if (ctas > 1) {
         const cudaError_t e = launch_dependent(attn::attention_combine_kernel<D>, dim3(ctas - 1, q.tile), dim3(D), 0, s, 1,
-                                               p, ctas, warps);
+                                               p, ctas);
         if (e != cudaSuccess) {
             tl_last_cuda_error = static_cast<int>(e);
             return I8R_ECUDA;
@@ -1304,7 +1304,8 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
 size_t int8_attention_decode_workspace_size(int Hq, int H, int D) {
     if (check_groups(Hq, H, D) != I8R_OK) return 0;
     const DecodeTiles q(Hq, H);
-    return align_up(2 * attn::DEC_MAX_CTAS * static_cast<size_t>(attn::piece_floats(q.tile, D)) * 4);
+    const size_t piece = static_cast<size_t>(attn::piece_floats(q.tile, D)) * 4;
+    return align_up(attn::DEC_MAX_CTAS * piece * (2 + (q.wide() ? attn::DEC_WARPS : 0)));
 }
 
 i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, int H, int D, const int8_t *Kc,
@@ -1320,6 +1321,7 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     I8R_TRY(check_ptr(O));
     I8R_TRY(check_index_ptr(lengths));
     I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
+    if (static_cast<long long>(num_blocks) * H > 0x7FFFFFFFll) return I8R_ERANGE;
     if (!workspace || workspace_bytes < int8_attention_decode_workspace_size(Hq, H, D)) return I8R_EWORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return I8R_EALIGN;
     const DeviceInfo *dev = nullptr;
@@ -1339,6 +1341,7 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     p.scale_log2 = std::fabs(scale) * 1.44269504088896340736f;      // log2(e)
     p.negate = scale < 0.0f ? 0x80008000u : 0u;
     p.part = static_cast<float *>(workspace);
+    p.firsts = p.part + 2ll * attn::DEC_MAX_CTAS * attn::piece_floats(q.tile, D);
     return D == 128 ? launch_decode_attention<128>(dev, p, q, stream) : launch_decode_attention<64>(dev, p, q, stream);
 }
 
