@@ -58,26 +58,25 @@ struct DecodeParams {
 
 // Floats of one piece: maximum, sum and D values per query.
 __host__ __device__ constexpr int piece_floats(int tile, int D) { return tile * (D + 2); }
-// Bytes of one warp's slots: four sub-tiles, K's and V's in turn; in the end its
-// last piece, which may be a little larger.
-__host__ __device__ constexpr int ring_bytes(int tile, int D) {
-    const int piece = (piece_floats(tile, D) * 4 + 15) / 16 * 16;
-    return piece > kv::BLOCK * D ? piece : kv::BLOCK * D;
-}
+// Bytes of one warp's slots: four sub-tiles, K's and V's in turn, or (two columns of
+// queries: fewer warps) eight, four for each.  In the end its last piece.
+__host__ __device__ constexpr int ring_bytes(int tile, int D) { return (tile > 8 ? 2 : 1) * kv::BLOCK * D; }
 // Bytes of one warp's queries, in the order of their MMA fragments.
 __host__ __device__ constexpr int query_bytes(int tile, int D) { return D / 16 * (tile > 8 ? 2 : 1) * 256; }
 __host__ __device__ constexpr size_t decode_smem(int tile, int D, int warps) {
     return static_cast<size_t>(warps) *
            (ring_bytes(tile, D) + query_bytes(tile, D) + (tile > 8 ? 0 : piece_floats(tile, D) * 4));
 }
-// Warps per CTA, one CTA an SM: 168 registers a lane.  (With two MMA columns of
-// queries that takes the queries' fragments out of registers, read from shared
-// memory for every 32 tokens; 8 warps of 255 registers were slower.)
-constexpr int DEC_WARPS = 12;
+// Warps per CTA, one CTA an SM: 12 of 168 registers a lane, or with two columns of
+// queries 8 of 255 (12, with the queries' fragments read from shared memory for
+// every 32 tokens, were slower: 289 us for 269 on 64 long sequences of 12 queries a head).
+__host__ __device__ constexpr int dec_warps(int nt) { return nt == 1 ? 12 : 8; }
+constexpr int DEC_MAX_WARPS = dec_warps(1);
 constexpr size_t DEC_SMEM = 226 * 1024;
-static_assert(decode_smem(8, 128, DEC_WARPS) <= DEC_SMEM && decode_smem(16, 128, DEC_WARPS) <= DEC_SMEM &&
-              decode_smem(8, 64, DEC_WARPS) <= DEC_SMEM && decode_smem(16, 64, DEC_WARPS) <= DEC_SMEM,
-              "the widest tiles fit");
+static_assert(decode_smem(8, 128, dec_warps(1)) <= DEC_SMEM && decode_smem(16, 128, dec_warps(2)) <= DEC_SMEM, "the widest tiles fit");
+static_assert(piece_floats(8, 64) * 4 <= ring_bytes(8, 64) && piece_floats(16, 64) * 4 <= ring_bytes(16, 64) &&
+              piece_floats(8, 128) * 4 <= ring_bytes(8, 128) && piece_floats(16, 128) * 4 <= ring_bytes(16, 128),
+              "a piece fits a warp's slots");
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // 8-byte asynchronous copy global -> shared; zeros instead with src_bytes = 0.
@@ -367,7 +366,7 @@ struct State {
     float m[NT][2], l[NT][2];            // of this lane's queries 2t, 2t + 1: the same in all its g
     float vs;                            // the scale acc is in (sV/127 of the last block with any)
     float start[NT][2];                  // -1152 sum(Q): what a score starts at
-    uint2 q[NT == 1 ? D / 16 : 1];       // the queries' fragments (NT = 1)
+    uint2 q[D / 16][NT];                 // the queries' fragments
 
     // a new item: nothing summed yet
     __device__ __forceinline__ void begin() {
@@ -386,21 +385,17 @@ struct State {
     }
 
     // its queries, once they have come
-    __device__ __forceinline__ void take_queries(const DecodeParams &p, uint8_t *queries) {
+    __device__ __forceinline__ void take_queries(const DecodeParams &p, const uint8_t *queries) {
         const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                uint2 *at = reinterpret_cast<uint2 *>(queries + (k * NT + n) * 256) + lane;
-                uint2 v = *at;
+                uint2 v = reinterpret_cast<const uint2 *>(queries + (k * NT + n) * 256)[lane];
                 v.x ^= p.negate;
                 v.y ^= p.negate;
-                if (NT == 1)
-                    q[k] = v;
-                else if (p.negate)
-                    *at = v;
+                q[k][n] = v;
                 const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
                 const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
                 sum += (a.x + a.y) + (b.x + b.y);
@@ -416,7 +411,7 @@ struct State {
     // codes of a word are the MMA's columns 2t, 2t+1, 2t+8, 2t+9 (so are the
     // queries').  Four chains of MMAs go side by side (two sub-tiles, and two halves
     // of each sum or two columns of queries): a chain alone waits for each MMA's result.
-    __device__ __forceinline__ void scores(const uint8_t *ring, const uint8_t *queries, int j, float (&x)[2][NT][4]) const {
+    __device__ __forceinline__ void scores(const uint8_t *ring, int j, float (&x)[2][NT][4]) const {
         float y[2][NT][4];
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -441,11 +436,6 @@ struct State {
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint2 f[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    f[n] = NT == 1 ? q[4 * c + k]
-                                   : reinterpret_cast<const uint2 *>(queries + ((4 * c + k) * NT + n) * 256)[lane];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t u = a[s][k] ^ 0x80808080u, v = b[s][k] ^ 0x80808080u;
@@ -453,7 +443,7 @@ struct State {
                     const uint32_t a1 = biased_codes<0x4140>(v), a3 = biased_codes<0x4342>(v);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816(NT == 1 && (k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, f[n].x, f[n].y);
+                        mma16816(NT == 1 && (k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, q[4 * c + k][n].x, q[4 * c + k][n].y);
                 }
             }
         }
@@ -604,15 +594,19 @@ struct Piece {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * DEC_WARPS, 1)
+__global__ void __launch_bounds__(32 * dec_warps(NT), 1)
     attention_decode_kernel(const __grid_constant__ DecodeParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Piece pieces[2 * DEC_WARPS];
+    __shared__ Piece pieces[2 * dec_warps(NT)];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int cta_warps = DEC_WARPS;
+    constexpr int cta_warps = dec_warps(NT);
     const int warp_ring = ring_bytes(p.tile, D);
     uint8_t *ring = smem + warp * warp_ring;
-    const uint32_t ring_u = smem_u32(ring);
+    // V's slots: K's own, filled in turn, or four more (kSplit)
+    constexpr bool kSplit = NT == 2;
+    constexpr int kAhead = kSplit ? SUBS - 1 : 1;        // groups of two sub-tiles that may be on the way at a wait
+    const uint32_t ring_u = smem_u32(ring), ring_v = ring_u + (kSplit ? SUBS * STEP * D : 0);
+    const uint8_t *v_slots = ring + (kSplit ? SUBS * STEP * D : 0);
     uint8_t *queries = smem + cta_warps * warp_ring + warp * query_bytes(p.tile, D);
     const uint32_t queries_u = smem_u32(queries);
     // a warp's first piece is written while its slots are still in use (a wide tile's
@@ -648,6 +642,14 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, 1)
                 if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
                 if (j & 1) cp_async_commit();
             }
+            if (kSplit) {
+                const int8_t *V = block_codes<D>(p.c.codes[1], slot);
+#pragma unroll
+                for (int j = 0; j < SUBS; ++j) {
+                    if (j >= j0 && j < j1) issue_v<D>(V, j, ring_v);
+                    if (j & 1) cp_async_commit();
+                }
+            }
         }
         float sk = __ldg(p.c.scale[0] + slot), sv = __ldg(p.c.scale[1] + slot);
         State<D, NT> st;
@@ -669,36 +671,55 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, 1)
                 sv_next = __ldg(p.c.scale[1] + slot_next);
             }
             const int i0 = w.step & (SUBS - 1), i1 = i0 + w.count;
+            const int j0 = ahead.step & (SUBS - 1), j1 = more ? j0 + ahead.count : 0;
+            auto next_k = [&](int j) {
+                const int8_t *K = block_codes<D>(p.c.codes[0], slot_next);
+                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
+                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
+            };
+            auto some_v = [&](int j, uint32_t at, int a, int e) {
+                const int8_t *V = block_codes<D>(p.c.codes[1], at);
+                if (j >= a && j < e) issue_v<D>(V, j, ring_v);
+                if (j + 1 >= a && j + 1 < e) issue_v<D>(V, j + 1, ring_v);
+            };
             float x[SUBS / 2][2][NT][4];
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
-                cp_async_wait<1>();
+                // a new item's queries came with its first K (kSplit: its last)
+                if (kSplit && fresh)
+                    cp_async_wait<kAhead - 1>();
+                else
+                    cp_async_wait<kAhead>();
                 if (j == 0 && fresh) st.take_queries(p, queries);
-                st.scores(ring, queries, j, x[j / 2]);
-                __syncwarp();                // read by all: the lanes copy V for one another
-                const int8_t *V = block_codes<D>(p.c.codes[1], slot);
-                if (j >= i0 && j < i1) issue_v<D>(V, j, ring_u);
-                if (j + 1 >= i0 && j + 1 < i1) issue_v<D>(V, j + 1, ring_u);
+                st.scores(ring, j, x[j / 2]);
+                if (kSplit) {
+                    if (j + 2 == SUBS && ends && more) issue_q<D, NT>(p, ahead, queries_u);
+                    next_k(j);
+                } else {
+                    __syncwarp();                // read by all: the lanes copy V for one another
+                    some_v(j, slot, i0, i1);
+                }
                 cp_async_commit();
             }
             const int lo = i0 * STEP;
             const int hi = min(lo + w.count * STEP, w.len - w.step / SUBS * kv::BLOCK);
             uint32_t pf[SUBS][NT][2];
             st.weigh(p, x, sk, sv, lo, hi, pf);
-            const int j0 = ahead.step & (SUBS - 1), j1 = more ? j0 + ahead.count : 0;
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
-                cp_async_wait<1>();
+                cp_async_wait<kAhead>();
                 __syncwarp();
                 if (sv != 0.0f) {
-                    st.values(ring, j, pf[j]);
-                    st.values(ring, j + 1, pf[j + 1]);
+                    st.values(v_slots, j, pf[j]);
+                    st.values(v_slots, j + 1, pf[j + 1]);
                 }
                 __syncwarp();
-                const int8_t *K = block_codes<D>(p.c.codes[0], slot_next);
-                if (j == 0 && ends && more) issue_q<D, NT>(p, ahead, queries_u);
-                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
-                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
+                if (kSplit) {
+                    some_v(j, slot_next, j0, j1);
+                } else {
+                    if (j == 0 && ends && more) issue_q<D, NT>(p, ahead, queries_u);
+                    next_k(j);
+                }
                 cp_async_commit();
             }
             fresh = ends;
@@ -794,9 +815,9 @@ __global__ void __launch_bounds__(32 * DEC_WARPS, 1)
 // the pieces of CTAs c, c + 1, ... up to the one where it ends.  One thread per
 // value; the pieces are read in order, eight at a time.  Launched as a
 // programmatic dependent: which item it is, is known from the lengths alone.
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas) {
-    constexpr int cta_warps = DEC_WARPS;
+    constexpr int cta_warps = dec_warps(NT);
     const int c = blockIdx.x, q = blockIdx.y, d = threadIdx.x;
     Steps order;
     order.load(p, ctas * cta_warps);

@@ -773,17 +773,18 @@ kv::Cache make_cache(const int8_t *Kc, const int8_t *Vc, const float *sK, const 
 
 template <int D>
 i8r_status launch_decode_attention(const DeviceInfo *dev, const attn::DecodeParams &p, const DecodeTiles &q, cudaStream_t s) {
-    constexpr int threads = 32 * attn::DEC_WARPS;
-    const size_t smem = attn::decode_smem(q.tile, D, attn::DEC_WARPS);
+    const int warps = attn::dec_warps(q.wide() ? 2 : 1);
+    const size_t smem = attn::decode_smem(q.tile, D, warps);
     const int ctas = std::min(dev->sms, attn::DEC_MAX_CTAS);
     if (q.wide())
-        attn::attention_decode_kernel<D, 2><<<ctas, threads, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 2><<<ctas, 32 * warps, smem, s>>>(p);
     else
-        attn::attention_decode_kernel<D, 1><<<ctas, threads, smem, s>>>(p);
+        attn::attention_decode_kernel<D, 1><<<ctas, 32 * warps, smem, s>>>(p);
     I8R_LAUNCHED();
     if (ctas > 1) {
-        const cudaError_t e = launch_dependent(attn::attention_combine_kernel<D>, dim3(ctas - 1, q.tile), dim3(D), 0, s, 1,
-                                               p, ctas);
+        const cudaError_t e = launch_dependent(
+            q.wide() ? attn::attention_combine_kernel<D, 2> : attn::attention_combine_kernel<D, 1>,
+            dim3(ctas - 1, q.tile), dim3(D), 0, s, 1, p, ctas);
         if (e != cudaSuccess) {
             tl_last_cuda_error = static_cast<int>(e);
             return I8R_ECUDA;
@@ -1305,7 +1306,7 @@ size_t int8_attention_decode_workspace_size(int Hq, int H, int D) {
     if (check_groups(Hq, H, D) != I8R_OK) return 0;
     const DecodeTiles q(Hq, H);
     const size_t piece = static_cast<size_t>(attn::piece_floats(q.tile, D)) * 4;
-    return align_up(attn::DEC_MAX_CTAS * piece * (2 + (q.wide() ? attn::DEC_WARPS : 0)));
+    return align_up(attn::DEC_MAX_CTAS * piece * (2 + (q.wide() ? attn::dec_warps(2) : 0)));
 }
 
 i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, int H, int D, const int8_t *Kc,
