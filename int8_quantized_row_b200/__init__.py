@@ -140,37 +140,99 @@ def _dev(t, dtype, name, ndim=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+# Argument checks of the decoder layer's operators.  They are on the path of every
+# token, so they ask a tensor for as little as they can (about 0.1 us a question)
+# and hand plain integers to ctypes.
+
+def _wrong(t, name, device, dtype):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, other arguments on cuda:{device}")
+
+
+def _at(t, name, device, dtype, shape):
+    """Address of a contiguous tensor of this device, type and shape."""
+    try:
+        if t.get_device() != device or t.dtype is not dtype:
+            _wrong(t, name, device, dtype)
+    except AttributeError:
+        _wrong(t, name, device, dtype)
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(first, *rest):
-    """The device of the tensor `first`, which every other tensor given has to be on."""
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    return first.device
+def _rows(t, name, device, dtype, shape):
+    """Address and row stride of a tensor [rows, heads, D] of this device, type and shape
+    whose rows may be strided (heads and their values contiguous)."""
+    try:
+        if t.get_device() != device or t.dtype is not dtype:
+            _wrong(t, name, device, dtype)
+    except AttributeError:
+        _wrong(t, name, device, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    n, H, D = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
+    row, head, value = t.stride()
+    if value != 1 or (H > 1 and head != D):
+        raise ValueError(f"{name}: heads and their values must be contiguous")
+    return t.data_ptr(), row if n > 1 else H * D
+
+
+def _device_of(t, name, ndim):
+    """Index of the CUDA device of a tensor of `ndim` dimensions."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    return t.get_device()
 
 
 class _on:
-    """Run with `device` current and allocations made on the stream the call uses, so that a
-    buffer freed at the end of the call is not handed out again before its kernels ran."""
+    """With this device current and, where the call names a stream, allocations made on that
+    stream: a buffer that the call frees at its end is not handed out again before its
+    kernels ran.  Gives the stream's handle."""
 
     def __init__(self, device, stream):
         import torch
-        self._device = torch.cuda.device(device)
-        self._stream = torch.cuda.stream(stream) if stream is not None else None
+        self._contexts = ()
+        if stream is not None:
+            if stream.device_index != device:
+                raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
+            self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
+            self._handle = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != device:
+                self._contexts = (torch.cuda.device(device),)
+            # current_stream(device).cuda_stream, without the 2 us of making a Stream
+            self._handle = torch._C._cuda_getCurrentRawStream(device)
 
     def __enter__(self):
-        self._device.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
+        for c in self._contexts:
+            c.__enter__()
+        return self._handle
 
     def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        self._device.__exit__(*exc)
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+
+
+def _workspace(workspace_buf, size, device):
+    """A buffer of `size` bytes, and its address and bytes; or the caller's."""
+    import torch
+    if workspace_buf is None:
+        workspace_buf = torch.empty(max(1, size), dtype=torch.uint8, device=device)
+    elif workspace_buf.get_device() != device.index:
+        _wrong(workspace_buf, "workspace_buf", device.index, workspace_buf.dtype)
+    return workspace_buf, workspace_buf.data_ptr(), workspace_buf.numel() * workspace_buf.element_size()
 
 
 def int8_quantize_weight_colwise(W16, Wq=None, sW=None, stream=None):
@@ -242,27 +304,22 @@ def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none
     import torch
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
-    x = _dev(X, torch.float16, "X", 2)
-    T, K = X.shape
-    wq = _dev(Wq, torch.int8, "Wq", 2)
-    N = Wq.shape[1]
-    _shape(Wq, (K, N), "Wq")
-    _shape(sW, (N,), "sW")
-    for t, name, shape in ((W16, "W16", (K, N)), (bias, "bias", (N,)), (residual, "residual", (T, N)), (Y, "Y", (T, N))):
-        if t is not None:
-            _shape(t, shape, name)
-    dev = _same_device(X, Wq, sW, W16, bias, residual, Y, workspace_buf)
-    opt = lambda t, name: _dev(t, torch.float16, name) if t is not None else _P()
-    with _on(dev, stream):
-        Y = torch.empty((T, N), dtype=torch.float16, device=dev) if Y is None else Y
-        if workspace_buf is None:
-            size = int8_mixed_linear_wq_workspace_size if W16 is None else int8_mixed_linear_workspace_size
-            workspace_buf = torch.empty(max(1, size(T, K, N)), dtype=torch.uint8, device=dev)
-        ws = workspace_buf
-        _check("int8_mixed_linear_fused", lib().int8_mixed_linear_fused(
-            x, T, K, wq, _dev(sW, torch.float32, "sW"), opt(W16, "W16"), N, float(alpha), opt(bias, "bias"),
-            ACTIVATIONS[act], opt(residual, "residual"), _dev(Y, torch.float16, "Y"),
-            ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)))
+    f16 = torch.float16
+    d = _device_of(X, "X", 2)
+    _device_of(Wq, "Wq", 2)
+    (T, K), N = X.shape, Wq.shape[1]
+    x, wq = _at(X, "X", d, f16, (T, K)), _at(Wq, "Wq", d, torch.int8, (K, N))
+    sw = _at(sW, "sW", d, torch.float32, (N,))
+    w16 = None if W16 is None else _at(W16, "W16", d, f16, (K, N))
+    b = None if bias is None else _at(bias, "bias", d, f16, (N,))
+    r = None if residual is None else _at(residual, "residual", d, f16, (T, N))
+    so = lib()
+    with _on(d, stream) as handle:
+        Y = torch.empty((T, N), dtype=f16, device=X.device) if Y is None else Y
+        size = so.int8_mixed_linear_wq_workspace_size if W16 is None else so.int8_mixed_linear_workspace_size
+        ws, at, nbytes = _workspace(workspace_buf, 0 if workspace_buf is not None else size(T, K, N), X.device)
+        _check("int8_mixed_linear_fused", so.int8_mixed_linear_fused(
+            x, T, K, wq, sw, w16, N, alpha, b, ACTIVATIONS[act], r, _at(Y, "Y", d, f16, (T, N)), at, nbytes, handle))
     return Y
 
 
@@ -461,36 +518,18 @@ def int4_linear(X, W4, S4, N, Y=None, workspace_buf=None, stream=None):
 
 # ---------------------------------------------------------------- the 8-bit key/value cache
 
-def _heads(t, name):
-    """fp16 [rows, heads, D] whose rows may be strided (heads and values contiguous):
-    its pointer and the elements from one row to the next."""
+def _cache_args(d, Kc, Vc, sK, sV, block_table):
+    """The C arguments of a cache on device d, checked: (Kc, Vc, sK, sV, num_blocks), (H, D),
+    (table, max_blocks), B."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dimensions")
-    n, H, D = t.shape
-    if t.numel() == 0 or n == 1 and t.is_contiguous():
-        return ctypes.c_void_p(t.data_ptr()), H * D
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name}: heads and their values must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else H * D
-
-
-def _cache_args(Kc, Vc, sK, sV, block_table):
-    """The C arguments of a cache, checked: (Kc, Vc, sK, sV, num_blocks), (H, D), (table, max_blocks)."""
-    import torch
-    kc = _dev(Kc, torch.int8, "Kc", 4)
-    blocks, H, tokens, D = Kc.shape
-    _shape(Kc, (blocks, H, KV_BLOCK, D), "Kc")
-    _shape(Vc, Kc.shape, "Vc")
-    _shape(sK, (blocks, H), "sK")
-    _shape(sV, (blocks, H), "sV")
-    table = _dev(block_table, torch.int32, "block_table", 2)
-    return ((kc, _dev(Vc, torch.int8, "Vc"), _dev(sK, torch.float32, "sK"), _dev(sV, torch.float32, "sV"), blocks),
-            (H, D), (table, block_table.shape[1]))
+    blocks, H, _, D = Kc.shape
+    codes, scales = (blocks, H, KV_BLOCK, D), (blocks, H)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have 2 dimensions")
+    B, wide = block_table.shape
+    return ((_at(Kc, "Kc", d, torch.int8, codes), _at(Vc, "Vc", d, torch.int8, codes),
+             _at(sK, "sK", d, torch.float32, scales), _at(sV, "sV", d, torch.float32, scales), blocks),
+            (H, D), (_at(block_table, "block_table", d, torch.int32, (B, wide)), wide), B)
 
 
 def int8_kv_append(K, V, cu_new, past, block_table, Kc, Vc, sK, sV, stream=None):
@@ -498,39 +537,35 @@ def int8_kv_append(K, V, cu_new, past, block_table, Kc, Vc, sK, sV, stream=None)
     of the cache (Kc, Vc int8 [blocks,H,64,D], sK, sV fp32 [blocks,H]), which holds past[b]
     tokens.  cu_new int32 [B+1], past int32 [B], block_table int32 [B,max_blocks]."""
     import torch
-    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
-    (k, ldk), (v, ldv) = _heads(K, "K"), _heads(V, "V")
-    _shape(K, (K.shape[0], H, D), "K")
-    _shape(V, K.shape, "V")
-    B = block_table.shape[0]
-    _shape(cu_new, (B + 1,), "cu_new")
-    _shape(past, (B,), "past")
-    with _on(_same_device(K, V, cu_new, past, block_table, Kc, Vc, sK, sV), stream):
-        _check("int8_kv_append", lib().int8_kv_append(
-            k, ldk, v, ldv, K.shape[0], H, D, _dev(cu_new, torch.int32, "cu_new"), _dev(past, torch.int32, "past"), B,
-            *cache, *table, _stream(stream)))
+    d = _device_of(Kc, "Kc", 4)
+    cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
+    _device_of(K, "K", 3)
+    rows = (K.shape[0], H, D)
+    k, ldk = _rows(K, "K", d, torch.float16, rows)
+    v, ldv = _rows(V, "V", d, torch.float16, rows)
+    cu, p = _at(cu_new, "cu_new", d, torch.int32, (B + 1,)), _at(past, "past", d, torch.int32, (B,))
+    with _on(d, stream) as handle:
+        _check("int8_kv_append", lib().int8_kv_append(k, ldk, v, ldv, rows[0], H, D, cu, p, B, *cache, *table, handle))
 
 
 def int8_kv_gather(Kc, Vc, sK, sV, cu, block_table, rows, K=None, V=None, stream=None):
     """-> (K, V) fp16 [rows,H,D]: tokens 0.. of sequence b of the cache in rows cu[b]..cu[b+1]-1
     (cu int32 [B+1]; rows behind cu[B] are not written)."""
     import torch
-    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
-    B = block_table.shape[0]
-    _shape(cu, (B + 1,), "cu")
+    d = _device_of(Kc, "Kc", 4)
+    cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
+    c = _at(cu, "cu", d, torch.int32, (B + 1,))
     shape = (int(rows), H, D)
-    for t, name in ((K, "K"), (V, "V")):
-        if t is not None:
-            _shape(t, shape, name)
-    dev = _same_device(Kc, Vc, sK, sV, cu, block_table, K, V)
-    with _on(dev, stream):
-        K = torch.empty(shape, dtype=torch.float16, device=dev) if K is None else K
-        V = torch.empty(shape, dtype=torch.float16, device=dev) if V is None else V
+    with _on(d, stream) as handle:
+        K = torch.empty(shape, dtype=torch.float16, device=Kc.device) if K is None else K
+        V = torch.empty(shape, dtype=torch.float16, device=Kc.device) if V is None else V
         _check("int8_kv_gather", lib().int8_kv_gather(
-            *cache, H, D, *table, _dev(cu, torch.int32, "cu"), B, shape[0], _dev(K, torch.float16, "K"),
-            _dev(V, torch.float16, "V"), _stream(stream)))
+            *cache, H, D, *table, c, B, shape[0], _at(K, "K", d, torch.float16, shape),
+            _at(V, "V", d, torch.float16, shape), handle))
     return K, V
 
+
+# ---------------------------------------------------------------- attention
 
 def int8_attention_decode_workspace_size(Hq, H, D):
     return int(lib().int8_attention_decode_workspace_size(int(Hq), int(H), int(D)))
@@ -540,25 +575,21 @@ def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O
     """O fp16 [B,Hq,D]: attention of one query token per sequence (Q fp16 [B,Hq,D], rows may be
     strided) over the first lengths[b] tokens of the 8-bit cache.  scale defaults to 1/sqrt(D)."""
     import torch
-    cache, (H, D), table = _cache_args(Kc, Vc, sK, sV, block_table)
-    q, ldq = _heads(Q, "Q")
-    B, Hq = Q.shape[0], Q.shape[1]
-    _shape(Q, (block_table.shape[0], Hq, D), "Q")
-    _shape(lengths, (B,), "lengths")
-    if O is not None:
-        _shape(O, Q.shape, "O")
-    dev = _same_device(Q, Kc, Vc, sK, sV, block_table, lengths, O, workspace_buf)
-    with _on(dev, stream):
-        O = torch.empty((B, Hq, D), dtype=torch.float16, device=dev) if O is None else O
-        if workspace_buf is None:
-            workspace_buf = torch.empty(max(1, int8_attention_decode_workspace_size(Hq, H, D)), dtype=torch.uint8,
-                                        device=dev)
-        ws = workspace_buf
-        o, ldo = _heads(O, "O")
-        _check("int8_attention_decode", lib().int8_attention_decode(
-            q, ldq, B, Hq, H, D, *cache, *table, _dev(lengths, torch.int32, "lengths"),
-            1.0 / D ** 0.5 if scale is None else float(scale), o, ldo, ctypes.c_void_p(ws.data_ptr()),
-            ws.numel() * ws.element_size(), _stream(stream)))
+    d = _device_of(Kc, "Kc", 4)
+    cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
+    _device_of(Q, "Q", 3)
+    Hq = Q.shape[1]
+    shape = (B, Hq, D)
+    q, ldq = _rows(Q, "Q", d, torch.float16, shape)
+    n = _at(lengths, "lengths", d, torch.int32, (B,))
+    so = lib()
+    with _on(d, stream) as handle:
+        O = torch.empty(shape, dtype=torch.float16, device=Q.device) if O is None else O
+        size = 0 if workspace_buf is not None else so.int8_attention_decode_workspace_size(Hq, H, D)
+        ws, at, nbytes = _workspace(workspace_buf, size, Q.device)
+        o, ldo = _rows(O, "O", d, torch.float16, shape)
+        _check("int8_attention_decode", so.int8_attention_decode(
+            q, ldq, B, Hq, H, D, *cache, *table, n, D ** -0.5 if scale is None else scale, o, ldo, at, nbytes, handle))
     return O
 
 
@@ -568,21 +599,20 @@ def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=N
     cu_k[b]..cu_k[b+1]-1 (cu_k defaults to cu_q), the last of each aligned.  scale defaults to
     1/sqrt(D).  Rows of O that belong to no sequence are not written."""
     import torch
-    cu_k = cu_q if cu_k is None else cu_k
-    (q, ldq), (k, ldk), (v, ldv) = _heads(Q, "Q"), _heads(K, "K"), _heads(V, "V")
-    (N, Hq, D), (M, H) = Q.shape, K.shape[:2]
-    _shape(K, (M, H, D), "K")
-    _shape(V, K.shape, "V")
-    B = cu_q.numel() - 1
-    _shape(cu_q, (max(B, 0) + 1,), "cu_q")
-    _shape(cu_k, cu_q.shape, "cu_k")
-    if O is not None:
-        _shape(O, Q.shape, "O")
-    dev = _same_device(Q, K, V, cu_q, cu_k, O)
-    with _on(dev, stream):
-        O = torch.empty((N, Hq, D), dtype=torch.float16, device=dev) if O is None else O
-        o, ldo = _heads(O, "O")
+    d = _device_of(Q, "Q", 3)
+    _device_of(K, "K", 3)
+    _device_of(cu_q, "cu_q", 1)
+    f16 = torch.float16
+    (N, Hq, D), (M, H, _) = Q.shape, K.shape
+    q, ldq = _rows(Q, "Q", d, f16, (N, Hq, D))
+    k, ldk = _rows(K, "K", d, f16, (M, H, D))
+    v, ldv = _rows(V, "V", d, f16, (M, H, D))
+    B = cu_q.shape[0] - 1
+    cq = _at(cu_q, "cu_q", d, torch.int32, (max(B, 0) + 1,))
+    ck = cq if cu_k is None else _at(cu_k, "cu_k", d, torch.int32, (B + 1,))
+    with _on(d, stream) as handle:
+        O = torch.empty((N, Hq, D), dtype=f16, device=Q.device) if O is None else O
+        o, ldo = _rows(O, "O", d, f16, (N, Hq, D))
         _check("int8_attention_prompt", lib().int8_attention_prompt(
-            q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, _dev(cu_q, torch.int32, "cu_q"), _dev(cu_k, torch.int32, "cu_k"), B,
-            1.0 / D ** 0.5 if scale is None else float(scale), o, ldo, _stream(stream)))
+            q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, D ** -0.5 if scale is None else scale, o, ldo, handle))
     return O
