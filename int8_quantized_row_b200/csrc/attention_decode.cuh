@@ -7,12 +7,11 @@
 //
 // Bound by reading the codes from HBM once (2 D bytes a token and head), so the
 // work is cut by bytes: an item is one (sequence, key/value head, tile of up to
-// 8*NT queries), all items' tokens in order are dealt in steps of 16 to the warps
-// of a persistent grid in equal contiguous ranges, and every warp works through
-// its range alone, a block of 64 tokens at a time (fewer at the range's ends).
-// Ranges usually begin and end inside an item; those pieces are merged per CTA in
-// shared memory, and the few items that cross CTAs by attention_combine_kernel
-// from at most two pieces a CTA, always in the same order.
+// 8*NT queries), the blocks of 64 tokens of all items in order are dealt to the warps
+// of a persistent grid in equal contiguous ranges, and every warp works through its
+// range alone.  Ranges usually begin and end inside an item; those pieces are merged
+// per CTA in shared memory, and the few items that cross CTAs by
+// attention_combine_kernel from at most two pieces a CTA, always in the same order.
 //
 // The codes travel by cp.async into the warp's own slots, four sub-tiles of 16
 // tokens: as K's are read, V's are asked for, and as V's are read, the next
@@ -39,9 +38,16 @@
 namespace i8r {
 namespace attn {
 
-constexpr int STEP = 16;                 // tokens per step: the granularity of the ranges
-constexpr int SUBS = kv::BLOCK / STEP;   // steps per block
+constexpr int STEP = 16;                 // tokens per sub-tile (an MMA's rows, or its depth)
+constexpr int SUBS = kv::BLOCK / STEP;   // sub-tiles per block
 constexpr int DEC_MAX_CTAS = 160;        // of the persistent grid (one per SM), which sizes the workspace
+
+// What attention_combine_kernel needs to know about a CTA: whether it had work, and
+// the item that begins in it and ends in another (b < 0: none), with the slot of its
+// piece there and the CTA where it ends.
+struct Join {
+    int b, h, gt, slot, last, worked;
+};
 
 struct DecodeParams {
     kv::Cache c;
@@ -54,6 +60,7 @@ struct DecodeParams {
     uint32_t negate;                     // sign bits that the queries are flipped by: scale < 0
     float *part;                         // [2 * CTAs][tile][D + 2]: pieces that cross CTAs
     float *firsts;                       // [warps of the grid][tile][D + 2]: warps' first pieces (wide tiles)
+    Join *joins;                         // [CTAs]
 };
 
 // Floats of one piece: maximum, sum and D values per query.
@@ -127,37 +134,54 @@ __device__ __forceinline__ int length_of(const DecodeParams &p, int b) {
     }
     return n;
 }
-// Where the steps of all items lie: sequence b's begin after those of the
-// sequences before it, H * GT items of item(len) steps each.  A lane keeps four
+// Blocks of one item of a sequence of n tokens.
+__device__ __forceinline__ int item_blocks(int n) { return (n + kv::BLOCK - 1) / kv::BLOCK; }
+
+// What a warp works on next: a block of the item (sequence b, key/value head h,
+// query tile gt).
+struct Place {
+    int b, h, gt, block, blocks, len;
+    // the block after this one; only called while the range has one
+    __device__ __forceinline__ void next(const DecodeParams &p) {
+        if (++block < blocks) return;
+        block = 0;
+        if (++gt < p.GT) return;
+        gt = 0;
+        if (++h < p.c.H) return;
+        h = 0;
+        do {
+            if (++b >= p.B) return;
+            len = length_of(p, b);
+        } while (len == 0);
+        blocks = item_blocks(len);
+    }
+};
+
+// Where the blocks of all items lie: sequence b's begin after those of the
+// sequences before it, H * GT items of item_blocks(len) each.  A lane keeps four
 // sequences' lengths of the first 128, which is all of them in most calls; more
-// are read again where they are needed.
-//
-// A warp takes about as long for one step of a block as for all four, so with at
-// least kCoarse blocks a warp every block counts whole and ranges are cut between
-// blocks; with fewer, ranges are cut between steps, so that more warps have work
-// (one sequence of 1000 tokens and 40 heads: 640 blocks, 2520 steps).
-struct Steps {
-    static constexpr int kCoarse = 4;
+// are read again where they are needed.  Ranges are cut between blocks: a warp
+// takes about as long for a part of one.
+struct Order {
     int len[4];
-    long long before;                    // steps of the sequences before this lane's four
+    long long before;                    // blocks of the sequences before this lane's four
     long long total;
     int warps;                           // of the grid
-    long long share;                     // units (blocks or steps) of a warp, and what is left over
+    long long share;                     // blocks of a warp, and what is left over
     int rest;
-    bool coarse;
 
-    __device__ __forceinline__ int item(int n) const { return item(n, coarse); }
-    __device__ __forceinline__ static int item(int n, bool coarse) {
-        return coarse ? (n + kv::BLOCK - 1) / kv::BLOCK * SUBS : (n + STEP - 1) / STEP;
-    }
     __device__ __forceinline__ static void lengths(const DecodeParams &p, int b0, int (&n)[4]) {
         const int b = b0 + 4 * (threadIdx.x & 31);
 #pragma unroll
         for (int j = 0; j < 4; ++j) n[j] = b + j < p.B ? length_of(p, b + j) : 0;
     }
-    __device__ __forceinline__ long long scan(const DecodeParams &p, const int (&n)[4], long long *prior) const {
+    __device__ __forceinline__ static long long blocks_of(const DecodeParams &p, const int (&n)[4]) {
+        return (static_cast<long long>(item_blocks(n[0])) + item_blocks(n[1]) + item_blocks(n[2]) + item_blocks(n[3])) *
+               (p.c.H * p.GT);
+    }
+    __device__ __forceinline__ static long long scan(const DecodeParams &p, const int (&n)[4], long long *prior) {
         const int lane = threadIdx.x & 31;
-        const long long mine = (static_cast<long long>(item(n[0])) + item(n[1]) + item(n[2]) + item(n[3])) * (p.c.H * p.GT);
+        const long long mine = blocks_of(p, n);
         long long sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -167,7 +191,9 @@ struct Steps {
         *prior = sum - mine;
         return __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    __device__ __forceinline__ void sum(const DecodeParams &p) {
+    __device__ __forceinline__ void load(const DecodeParams &p, int grid_warps) {
+        warps = grid_warps;
+        lengths(p, 0, len);
         total = scan(p, len, &before);
         for (int b0 = 128; b0 < p.B; b0 += 128) {
             int n[4];
@@ -175,29 +201,19 @@ struct Steps {
             lengths(p, b0, n);
             total += scan(p, n, &prior);
         }
+        share = total / warps;
+        rest = static_cast<int>(total - share * warps);
     }
-    __device__ __forceinline__ void load(const DecodeParams &p, int grid_warps) {
-        warps = grid_warps;
-        lengths(p, 0, len);
-        coarse = true;
-        sum(p);
-        if (total < static_cast<long long>(kCoarse) * SUBS * warps) {
-            coarse = false;
-            sum(p);
-        }
-        const long long units = coarse ? total / SUBS : total;
-        share = units / warps;
-        rest = static_cast<int>(units - share * warps);
-    }
-    // The first step of warp w's range: floor(units * w / warps) units.
+    // The first block of warp w's range, floor(total * w / warps), and the warp whose range holds block u.
     __device__ __forceinline__ long long begin(int w) const {
-        const long long u = share * w + static_cast<unsigned>(rest * w) / static_cast<unsigned>(warps);
-        return coarse ? u * SUBS : u;
+        return share * w + static_cast<unsigned>(rest * w) / static_cast<unsigned>(warps);
     }
-    // The sequence (and its length), item and step of step u < total.
-    __device__ __forceinline__ void find(const DecodeParams &p, long long u, int *b, int *n, int *hg, int *step) const {
+    __device__ __forceinline__ int owner(long long u) const {
+        return static_cast<int>(((u + 1) * warps - 1) / total);
+    }
+    // Block u < total.
+    __device__ __forceinline__ void find(const DecodeParams &p, long long u, Place *w) const {
         const int lane = threadIdx.x & 31;
-        const long long items = static_cast<long long>(p.c.H) * p.GT;
         int v[4] = {len[0], len[1], len[2], len[3]};
         long long prior = before, base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 128) {
@@ -205,7 +221,7 @@ struct Steps {
                 lengths(p, b0, v);
                 scan(p, v, &prior);
             }
-            const long long mine = (static_cast<long long>(item(v[0])) + item(v[1]) + item(v[2]) + item(v[3])) * items;
+            const long long mine = blocks_of(p, v);
             long long r = u - base - prior;                          // within this lane's four sequences
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, r >= 0 && r < mine);
             if (hit) {
@@ -213,53 +229,23 @@ struct Steps {
                 int k = 0;
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
-                    const long long c = item(v[j]) * items;
+                    const long long c = static_cast<long long>(item_blocks(v[j])) * (p.c.H * p.GT);
                     if (k == j && r >= c) r -= c, k = j + 1;
                 }
                 const int own = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
-                r = __shfl_sync(0xFFFFFFFFu, r, at);
-                *n = __shfl_sync(0xFFFFFFFFu, own, at);
-                *b = __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + k, at);
-                *hg = static_cast<int>(r / item(*n));
-                *step = static_cast<int>(r - static_cast<long long>(*hg) * item(*n));
+                // within one sequence: at most 2^31 blocks, as the cache has (32-bit slots)
+                const unsigned in = static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, r, at));
+                w->len = __shfl_sync(0xFFFFFFFFu, own, at);
+                w->b = __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + k, at);
+                w->blocks = item_blocks(w->len);
+                const unsigned hg = in / static_cast<unsigned>(w->blocks);
+                w->block = static_cast<int>(in - hg * w->blocks);
+                w->h = static_cast<int>(hg / p.GT);
+                w->gt = static_cast<int>(hg % p.GT);
                 return;
             }
             base += __shfl_sync(0xFFFFFFFFu, prior + mine, 31);
         }
-    }
-};
-
-// What a warp works on next: steps [step, step + count) of the item (sequence b,
-// key/value head h, query tile gt), all in one block.
-struct Place {
-    int b, h, gt, step, count, steps, len;
-    bool coarse;
-    __device__ __forceinline__ void at(const DecodeParams &p, const Steps &order, long long u) {
-        int hg;
-        order.find(p, u, &b, &len, &hg, &step);
-        steps = order.item(len);
-        h = hg / p.GT;
-        gt = hg % p.GT;
-        coarse = order.coarse;
-    }
-    // the rest of the block that `step` lies in, of the item, and of the range
-    __device__ __forceinline__ void cut(int left) {
-        count = min(left, min(SUBS - (step & (SUBS - 1)), steps - step));
-    }
-    // the step after these; only called while the range has one
-    __device__ __forceinline__ void next(const DecodeParams &p) {
-        step += count;
-        if (step < steps) return;
-        step = 0;
-        if (++gt < p.GT) return;
-        gt = 0;
-        if (++h < p.c.H) return;
-        h = 0;
-        do {
-            if (++b >= p.B) return;
-            len = length_of(p, b);
-        } while (len == 0);
-        steps = Steps::item(len, coarse);
     }
 };
 
@@ -271,7 +257,7 @@ struct Window {
     // where a place's block and head lie, in blocks of one head (the host checks that
     // 32 bits hold them); a bad block number (reported) reads block 0, which is always there
     __device__ __forceinline__ uint32_t slot(const DecodeParams &p, const Place &w) {
-        const int i = w.step / SUBS;
+        const int i = w.block;
         if (w.b != b || i < first || i >= first + 32) {
             b = w.b;
             first = i & ~31;
@@ -457,16 +443,16 @@ struct State {
 
     // The block's scores become weights (in `pf`, as the second product's
     // fragments), the maxima and sums move on, and acc is rescaled to them and to
-    // the block's V scale.  Tokens outside [lo, hi) of the block weigh nothing.
-    __device__ __forceinline__ void weigh(const DecodeParams &p, float (&x)[SUBS / 2][2][NT][4], float sk, float sv, int lo,
-                                          int hi, uint32_t (&pf)[SUBS][NT][2]) {
+    // the block's V scale.  Tokens from hi on weigh nothing.
+    __device__ __forceinline__ void weigh(const DecodeParams &p, float (&x)[SUBS / 2][2][NT][4], float sk, float sv, int hi,
+                                          uint32_t (&pf)[SUBS][NT][2]) {
         const int g = (threadIdx.x & 31) >> 2;
         const float ks = p.scale_log2 * (sk * (1.0f / 127.0f)), now = sv * (1.0f / 127.0f);
         // a block whose scale is 0 stands for zeros, whatever its codes: values() is not called for it
         const bool nothing = now == 0.0f;
         const float turn = nothing ? 1.0f : vs / now;
         if (!nothing) vs = now;
-        const bool cut = lo > 0 || hi < kv::BLOCK;
+        const bool cut = hi < kv::BLOCK;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float keep[2], alpha[2];
@@ -478,8 +464,8 @@ struct State {
                     float &u = x[j >> 1][j & 1][n][e], &v = x[j >> 1][j & 1][n][2 + e];
                     if (cut) {
                         const int t0 = STEP * j + g;
-                        u = t0 >= lo && t0 < hi ? u : -INFINITY;
-                        v = t0 + 8 >= lo && t0 + 8 < hi ? v : -INFINITY;
+                        u = t0 < hi ? u : -INFINITY;
+                        v = t0 + 8 < hi ? v : -INFINITY;
                     }
                     top = fmaxf(top, fmaxf(u, v));
                 }
@@ -589,8 +575,9 @@ struct State {
 // What a warp left of an item it did not do alone.
 struct Piece {
     int b, h, gt;                        // b < 0: none
-    bool starts, ends;                   // the piece holds the item's first / last step
+    bool starts;                         // the piece holds the item's first block
     bool front;                          // it begins where the CTA's range begins
+    int left;                            // blocks of the item after it
 };
 
 template <int D, int NT>
@@ -615,38 +602,40 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
                             : p.firsts + static_cast<size_t>(blockIdx.x) * cta_warps * piece_floats(p.tile, D);
     if (lane < 2) pieces[2 * warp + lane].b = -1;
     __syncwarp();
-    griddep_launch_dependents();         // combine_kernel may find its items meanwhile (it fits in beside no CTA of this grid)
+    griddep_wait();                      // what the lengths, the cache and the queries come from
+    griddep_launch_dependents();         // the combining blocks may take the SMs' places as CTAs leave
 
     Place w, ahead;
-    long long u0, u1;
+    long long u0, u1, total, cta_end;
     bool front;
     {
-        Steps order;
+        Order order;
         order.load(p, gridDim.x * cta_warps);
-        u0 = order.begin(blockIdx.x * cta_warps + warp);
-        u1 = order.begin(blockIdx.x * cta_warps + warp + 1);
+        const int me = blockIdx.x * cta_warps + warp;
+        u0 = order.begin(me);
+        u1 = order.begin(me + 1);
         front = u0 == order.begin(blockIdx.x * cta_warps);
-        if (u0 < u1) w.at(p, order, u0);
+        cta_end = order.begin((blockIdx.x + 1) * cta_warps);
+        total = order.total;
+        if (u0 < u1) order.find(p, u0, &w);
     }
     if (u0 < u1) {
-        int left = static_cast<int>(min(u1 - u0, 0x7FFFFFFFll));      // steps of the range from w on
-        w.cut(left);
+        int left = static_cast<int>(u1 - u0) - 1;                     // blocks of the range after w
         Window window;
         uint32_t slot = window.slot(p, w), slot_next = 0;
         issue_q<D, NT>(p, w, queries_u);
         {
             const int8_t *K = block_codes<D>(p.c.codes[0], slot);
-            const int j0 = w.step & (SUBS - 1), j1 = j0 + w.count;
 #pragma unroll
             for (int j = 0; j < SUBS; ++j) {
-                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
+                issue_k<D>(K, j, ring_u);
                 if (j & 1) cp_async_commit();
             }
             if (kSplit) {
                 const int8_t *V = block_codes<D>(p.c.codes[1], slot);
 #pragma unroll
                 for (int j = 0; j < SUBS; ++j) {
-                    if (j >= j0 && j < j1) issue_v<D>(V, j, ring_v);
+                    issue_v<D>(V, j, ring_v);
                     if (j & 1) cp_async_commit();
                 }
             }
@@ -654,33 +643,30 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
         float sk = __ldg(p.c.scale[0] + slot), sv = __ldg(p.c.scale[1] + slot);
         State<D, NT> st;
         st.begin();
-        left -= w.count;
         ahead = w;
         if (left > 0) {
             ahead.next(p);
-            ahead.cut(left);
             slot_next = window.slot(p, ahead);
         }
-        bool starts = w.step == 0, first = true, fresh = true;
+        bool starts = w.block == 0, first = true, fresh = true;
         while (true) {
             // the block after this one: its scales now, its codes as the slots come free
-            const bool more = left > 0, ends = w.step + w.count == w.steps;
+            const bool more = left > 0, ends = w.block + 1 == w.blocks;
             float sk_next = 0.0f, sv_next = 0.0f;
             if (more) {
                 sk_next = __ldg(p.c.scale[0] + slot_next);
                 sv_next = __ldg(p.c.scale[1] + slot_next);
             }
-            const int i0 = w.step & (SUBS - 1), i1 = i0 + w.count;
-            const int j0 = ahead.step & (SUBS - 1), j1 = more ? j0 + ahead.count : 0;
             auto next_k = [&](int j) {
+                if (!more) return;
                 const int8_t *K = block_codes<D>(p.c.codes[0], slot_next);
-                if (j >= j0 && j < j1) issue_k<D>(K, j, ring_u);
-                if (j + 1 >= j0 && j + 1 < j1) issue_k<D>(K, j + 1, ring_u);
+                issue_k<D>(K, j, ring_u);
+                issue_k<D>(K, j + 1, ring_u);
             };
-            auto some_v = [&](int j, uint32_t at, int a, int e) {
+            auto some_v = [&](int j, uint32_t at) {
                 const int8_t *V = block_codes<D>(p.c.codes[1], at);
-                if (j >= a && j < e) issue_v<D>(V, j, ring_v);
-                if (j + 1 >= a && j + 1 < e) issue_v<D>(V, j + 1, ring_v);
+                issue_v<D>(V, j, ring_v);
+                issue_v<D>(V, j + 1, ring_v);
             };
             float x[SUBS / 2][2][NT][4];
 #pragma unroll
@@ -697,14 +683,12 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
                     next_k(j);
                 } else {
                     __syncwarp();                // read by all: the lanes copy V for one another
-                    some_v(j, slot, i0, i1);
+                    some_v(j, slot);
                 }
                 cp_async_commit();
             }
-            const int lo = i0 * STEP;
-            const int hi = min(lo + w.count * STEP, w.len - w.step / SUBS * kv::BLOCK);
             uint32_t pf[SUBS][NT][2];
-            st.weigh(p, x, sk, sv, lo, hi, pf);
+            st.weigh(p, x, sk, sv, min(kv::BLOCK, w.len - w.block * kv::BLOCK), pf);
 #pragma unroll
             for (int j = 0; j < SUBS; j += 2) {
                 cp_async_wait<kAhead>();
@@ -715,7 +699,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
                 }
                 __syncwarp();
                 if (kSplit) {
-                    some_v(j, slot_next, j0, j1);
+                    if (more) some_v(j, slot_next);
                 } else {
                     if (j == 0 && ends && more) issue_q<D, NT>(p, ahead, queries_u);
                     next_k(j);
@@ -726,7 +710,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
             if (ends || !more) {
                 const bool whole = starts && ends;
                 if (!whole && lane == 0)
-                    pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.h, w.gt, starts, ends, first && front};
+                    pieces[2 * warp + (first ? 0 : 1)] = Piece{w.b, w.h, w.gt, starts, first && front, w.blocks - 1 - w.block};
                 st.end(p, w, whole, first ? firsts + warp * piece_floats(p.tile, D) : reinterpret_cast<float *>(ring));
                 first = false;
                 starts = true;
@@ -737,10 +721,8 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
             slot = slot_next;
             sk = sk_next;
             sv = sv_next;
-            left -= w.count;
-            if (left > 0) {
+            if (--left > 0) {
                 ahead.next(p);
-                ahead.cut(left);
                 slot_next = window.slot(p, ahead);
             }
         }
@@ -754,6 +736,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
         return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)
                        : firsts + (k >> 1) * piece_floats(p.tile, D);
     };
+    bool joined = false;
     for (int i = 0; i < 2 * cta_warps;) {
         const Piece a = pieces[i];
         if (a.b < 0) {
@@ -766,8 +749,15 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
             if (pieces[j].b != a.b || pieces[j].h != a.h || pieces[j].gt != a.gt) break;
             last = j;
         }
-        const bool whole = a.starts && pieces[last].ends;
+        const bool whole = a.starts && pieces[last].left == 0;
         const int out_slot = a.front ? 0 : 1;
+        // an item that goes on in other CTAs (the last one here, if any)
+        if (a.starts && pieces[last].left > 0 && threadIdx.x == 0) {
+            const long long end = cta_end + pieces[last].left - 1;
+            const int ends_in = static_cast<int>(((end + 1) * (gridDim.x * cta_warps) - 1) / total) / cta_warps;
+            p.joins[blockIdx.x] = Join{a.b, a.h, a.gt, out_slot, ends_in, 1};
+            joined = true;
+        }
         float *out = p.part + static_cast<size_t>(2 * blockIdx.x + out_slot) * piece_floats(p.tile, D);
         const int h = a.h, q0 = a.gt * p.tile;
         const int nq = min(p.tile, p.G - q0);
@@ -803,6 +793,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
         }
         i = j;
     }
+    if (threadIdx.x == 0 && !joined) p.joins[blockIdx.x] = Join{-1, 0, 0, 0, 0, u0 < cta_end ? 1 : 0};
     // sequences without tokens
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)
         if (length_of(p, b) == 0)
@@ -810,42 +801,32 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
                 *reinterpret_cast<uint4 *>(p.O + static_cast<size_t>(b) * p.ldo + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The items that cross CTAs.  Block (c, q): if the range of CTA c + 1 begins
-// inside an item that began in CTA c's range, that item's query q is the sum of
-// the pieces of CTAs c, c + 1, ... up to the one where it ends.  One thread per
-// value; the pieces are read in order, eight at a time.  Launched as a
-// programmatic dependent: which item it is, is known from the lengths alone.
-template <int D, int NT>
-__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p, int ctas) {
-    constexpr int cta_warps = dec_warps(NT);
-    const int c = blockIdx.x, q = blockIdx.y, d = threadIdx.x;
-    Steps order;
-    order.load(p, ctas * cta_warps);
-    auto begin = [&](int cta) { return order.begin(cta * cta_warps); };
-    const long long u = begin(c + 1);
-    Place w;
-    w.step = w.steps = w.gt = 0;
-    if (u < order.total) w.at(p, order, u);
-    // every block waits, also one without an item: the kernels after this one in
-    // the stream wait for this grid alone
+// The items that cross CTAs.  Block (c, q): query q of the item that begins in CTA
+// c's range and ends in a later one's is the sum of the pieces of those CTAs.  One
+// thread per value; the pieces are read in order, eight at a time.
+template <int D>
+__global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_constant__ DecodeParams p) {
+    // every block waits, also one without an item: the kernels after this one in the
+    // stream wait for this grid alone
     griddep_wait();
-    const long long start = u - w.step, end = start + w.steps;
-    const int q0 = w.gt * p.tile;
-    if (w.step == 0 || start < begin(c) || q0 + q >= p.G) return;
-    auto row = [&](int cta) {
-        const int slot = start <= begin(cta) ? 0 : 1;
-        return piece_row<D>(p.part + static_cast<size_t>(2 * cta + slot) * piece_floats(p.tile, D), q);
-    };
+    griddep_launch_dependents();
+    const int c = blockIdx.x, q = blockIdx.y, d = threadIdx.x;
+    const Join join = p.joins[c];
+    const int q0 = join.gt * p.tile;
+    if (join.b < 0 || q0 + q >= p.G) return;
     float top = -INFINITY, sum = 0.0f, o = 0.0f;
-    for (int k0 = c; k0 < ctas && begin(k0) < end; k0 += 8) {
+    for (int k0 = c; k0 <= join.last; k0 += 8) {
         float m[8], l[8], v[8], was = top;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+            // in the CTAs after the first it begins where their ranges do; a CTA without
+            // blocks (fewer blocks than CTAs) has no piece
+            const int cta = k0 + k;
             m[k] = -INFINITY;
             l[k] = v[k] = 0.0f;
-            // a CTA without steps (fewer steps than warps) has no piece
-            if (k0 + k < ctas && begin(k0 + k) < min(end, begin(k0 + k + 1))) {
-                const float *r = row(k0 + k);
+            if (cta <= join.last && p.joins[cta].worked) {
+                const float *r = piece_row<D>(
+                    p.part + static_cast<size_t>(2 * cta + (cta == c ? join.slot : 0)) * piece_floats(p.tile, D), q);
                 m[k] = __ldcg(r);
                 l[k] = __ldcg(r + 1);
                 v[k] = __ldcg(r + 2 + d);
@@ -863,7 +844,7 @@ __global__ void __launch_bounds__(D) attention_combine_kernel(const __grid_const
             o = fmaf(wgt, v[k], o);
         }
     }
-    p.O[static_cast<size_t>(w.b) * p.ldo + static_cast<size_t>(w.h * p.G + q0 + q) * D + d] = __float2half_rn(o / sum);
+    p.O[static_cast<size_t>(join.b) * p.ldo + static_cast<size_t>(join.h * p.G + q0 + q) * D + d] = __float2half_rn(o / sum);
 }
 
 }  // namespace attn

@@ -776,21 +776,18 @@ i8r_status launch_decode_attention(const DeviceInfo *dev, const attn::DecodePara
     const int warps = attn::dec_warps(q.wide() ? 2 : 1);
     const size_t smem = attn::decode_smem(q.tile, D, warps);
     const int ctas = std::min(dev->sms, attn::DEC_MAX_CTAS);
-    if (q.wide())
-        attn::attention_decode_kernel<D, 2><<<ctas, 32 * warps, smem, s>>>(p);
-    else
-        attn::attention_decode_kernel<D, 1><<<ctas, 32 * warps, smem, s>>>(p);
-    I8R_LAUNCHED();
-    if (ctas > 1) {
-        const cudaError_t e = launch_dependent(
-            q.wide() ? attn::attention_combine_kernel<D, 2> : attn::attention_combine_kernel<D, 1>,
-            dim3(ctas - 1, q.tile), dim3(D), 0, s, 1, p, ctas);
-        if (e != cudaSuccess) {
-            tl_last_cuda_error = static_cast<int>(e);
-            return I8R_ECUDA;
-        }
+    cudaError_t e = launch_dependent(q.wide() ? attn::attention_decode_kernel<D, 2> : attn::attention_decode_kernel<D, 1>,
+                                     dim3(ctas), dim3(32 * warps), smem, s, 1, p);
+    if (e == cudaSuccess) {
         I8R_LAUNCHED();
+        if (ctas == 1) return I8R_OK;            // nothing to join
+        e = launch_dependent(attn::attention_combine_kernel<D>, dim3(ctas - 1, q.tile), dim3(D), 0, s, 1, p);
     }
+    if (e != cudaSuccess) {
+        tl_last_cuda_error = static_cast<int>(e);
+        return I8R_ECUDA;
+    }
+    I8R_LAUNCHED();
     return I8R_OK;
 }
 
@@ -1306,7 +1303,7 @@ size_t int8_attention_decode_workspace_size(int Hq, int H, int D) {
     if (check_groups(Hq, H, D) != I8R_OK) return 0;
     const DecodeTiles q(Hq, H);
     const size_t piece = static_cast<size_t>(attn::piece_floats(q.tile, D)) * 4;
-    return align_up(attn::DEC_MAX_CTAS * piece * (2 + (q.wide() ? attn::dec_warps(2) : 0)));
+    return align_up(attn::DEC_MAX_CTAS * (piece * (2 + (q.wide() ? attn::dec_warps(2) : 0)) + sizeof(attn::Join)));
 }
 
 i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, int H, int D, const int8_t *Kc,
@@ -1342,7 +1339,9 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     p.scale_log2 = std::fabs(scale) * 1.44269504088896340736f;      // log2(e)
     p.negate = scale < 0.0f ? 0x80008000u : 0u;
     p.part = static_cast<float *>(workspace);
-    p.firsts = p.part + 2ll * attn::DEC_MAX_CTAS * attn::piece_floats(q.tile, D);
+    const size_t piece = static_cast<size_t>(attn::piece_floats(q.tile, D));
+    p.firsts = p.part + 2 * attn::DEC_MAX_CTAS * piece;
+    p.joins = reinterpret_cast<attn::Join *>(p.firsts + (q.wide() ? attn::DEC_MAX_CTAS * attn::dec_warps(2) * piece : 0));
     return D == 128 ? launch_decode_attention<128>(dev, p, q, stream) : launch_decode_attention<64>(dev, p, q, stream);
 }
 
