@@ -26,8 +26,13 @@
 // cuts, the tile's warps look for infinities and NaN among V's rows; where there
 // is one, that step's P V is summed by the warps over the visible keys alone.
 //
-// Roles: warps 0-3 and 4-7 the tiles' softmax, warp 8 the TMA producer, warp 9
-// the MMA issuer.  Every wait is bounded (timeout -> device status word).
+// CTAs are persistent and everything crosses from one 256-row piece of work to the
+// next: the next Q, K and V are loaded and its first scores computed while the last
+// one's sums are scaled and stored.  Roles: warps 0-3 and 4-7 the two tiles' softmax,
+// 8 the TMA producer, 9 the MMA issuer (the whole warp in step, so that operands stay
+// in uniform registers; with one lane in a branch an MMA took 140 cycles to issue, of
+// the 64 it runs), 10 looks over V for what a mask must hide, 11 finds the work.
+// Every wait is bounded (timeout -> device status word).
 #pragma once
 
 #include "attention_decode.cuh"
@@ -39,17 +44,23 @@ namespace attn {
 
 constexpr int PT = 128;                        // query rows per tile, keys per step
 constexpr int PROMPT_ROWS = 2 * PT;            // query rows per CTA
-constexpr int PROMPT_THREADS = 320;
+constexpr int PROMPT_THREADS = 384;            // 8 softmax warps and four others
+// Registers: 384 threads are launched with 168 each; the softmax warps take 224
+// (a row's 128 scores stay in them) and the other four 56.
+constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 224, OTHER_REGS = 56;
+static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * 128 <= PROMPT_LAUNCH_REGS * PROMPT_THREADS, "more registers than launched with");
 constexpr uint32_t PROMPT_TMEM = 512;
 constexpr float RAISE = 8.0f;                  // log2 of how far a row may exceed its reference
+
+constexpr int OUT_BYTES = 32 * 128;            // a softmax warp's rows on their way out, 64 columns at a time
 
 template <int D>
 struct PromptShape {
     static constexpr int CHUNKS = D / 64;                      // 128-byte swizzle spans of a row
     static constexpr int CHUNK_BYTES = PT * 128;
     static constexpr int TILE_BYTES = CHUNKS * CHUNK_BYTES;    // a Q, K or V tile
-    static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 512;
+    static constexpr int STAGES = D == 128 ? 4 : 10;
+    static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 8 * OUT_BYTES + 512;
 };
 
 struct PromptParams {
@@ -61,14 +72,32 @@ struct PromptParams {
     uint32_t negate;                           // idesc bit: scale < 0
 };
 
+// 256 query rows of one (sequence, head).
+struct PromptWork {
+    int row, rows;                             // first row of Q and O; rows of the sequence from there on
+    int key, head;                             // first row of K and V
+    int seen;                                  // the last of the sequence's keys that the first row sees (may be < 0)
+    int steps[2];                              // steps of 128 keys for each tile; -1: no more work
+};
+// The first step that the mask cuts for a tile whose first row sees keys up to `seen`;
+// from the first tile's on there are at most kCuts steps.
+constexpr int kCuts = 3;
+__device__ __forceinline__ int first_cut(int seen) { return seen + 1 > 0 ? (seen + 1) / PT : 0; }
+
+// Barriers that complete once per piece of work have parity (work & 1); those of the
+// two work slots (work >> 1) & 1.
 struct PromptBarriers {
     uint64_t full[10], empty[10];              // the K/V ring
-    uint64_t q_full;
-    uint64_t s_full[2], p_ready[2], o_full[2], scan[2];
+    uint64_t q_full[2], q_empty[2];            // a tile's queries
+    uint64_t s_full[2], p_ready[2][2];         // scores; P: tile, half of the keys (once per step)
+    uint64_t o_full[2], o_empty[2];            // the sums
+    uint64_t asked[2][kCuts], scan[2][kCuts];  // V of a cut step: asked for, looked over (work slot, cut)
+    uint64_t work_full[2], work_empty[2];
     uint64_t drain;
+    PromptWork work[2];
     uint32_t tmem_base;
     int abort;
-    int dirty_step[2], skip_step[2];
+    int dirty[2][kCuts], skip[2];              // a cut step's V is not finite; the step (counted through) whose P V is done
 };
 static_assert(sizeof(PromptBarriers) <= 512, "barrier block outgrew its shared-memory reserve");
 
@@ -101,6 +130,37 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
 }
 
+// The MMAs with descriptors given as their low halves (address and leading
+// dimension; the high half is the same for every operand here): one addition an
+// operand.  Called by a whole warp; one lane issues.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);    // 8 rows 1024 B apart, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t address, uint32_t lbo) { return (address >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+        "r"(accumulate), "r"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a_tmem), "r"(b), "r"(idesc),
+        "r"(accumulate), "r"(kDescHigh)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_elected(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
 // Whether any of eight fp16 values is an infinity or NaN (exponent all ones).
 __device__ __forceinline__ bool not_finite(const uint4 &v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -111,6 +171,50 @@ __device__ __forceinline__ bool not_finite(const uint4 &v) {
     return bad;
 }
 
+// P V of one step over the keys that each row sees, without the tensor cores: O (in
+// tensor memory at t_o; zeros before the first step) += sum over keys 0 .. seen of
+// this lane's P (at t_s) and V's rows (128-byte-swizzled 64-column chunks).  For the
+// rare step whose V holds infinities or NaN that some rows do not see.
+template <int D>
+__device__ __forceinline__ void values_seen(uint32_t t_s, uint32_t t_o, const uint8_t *v, bool accumulate, int seen) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+        if (accumulate) {
+            tmem_ld32(t_o + 32 * c, o);
+            tmem_wait_ld();
+        }
+#pragma unroll 1
+        for (int k = 0; k < PT; ++k) {
+            uint32_t pp;
+            tmem_ld1(t_s + k / 2, pp);
+            tmem_wait_ld();
+            const float2 pf = __half22float2(*reinterpret_cast<const __half2 *>(&pp));
+            if (k <= seen) {
+                const float pk = (k & 1) ? pf.y : pf.x;
+                const uint8_t *src = v + (c >> 1) * PromptShape<D>::CHUNK_BYTES + k * 128;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(src + (((4 * (c & 1) + u) ^ (k & 7)) << 4));
+                    const __half2 *hv = reinterpret_cast<const __half2 *>(&q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = __half22float2(hv[e]);
+                        uint32_t &o0 = o[8 * u + 2 * e], &o1 = o[8 * u + 2 * e + 1];
+                        o0 = __float_as_uint(fmaf(pk, f.x, __uint_as_float(o0)));
+                        o1 = __float_as_uint(fmaf(pk, f.y, __uint_as_float(o1)));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        tmem_st32(t_o + 32 * c, o);
+    }
+    tmem_wait_st();
+}
+
 template <int D>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1)
     attention_prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -118,51 +222,41 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
     using Shape = PromptShape<D>;
     constexpr int STAGES = Shape::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    // The longest tiles of a sequence first; neighbouring CTAs are the heads of one
-    // tile, which share keys and values.
-    const int head = blockIdx.x % p.Hq;
-    long long place = 0;
-    auto tiles = [&](int s) {
-        const int2 r = kv::row_range(p.cu_q, s, p.N);
-        return (r.y - r.x + PROMPT_ROWS - 1) / PROMPT_ROWS;
-    };
-    const int b = kv::find_item(blockIdx.x / p.Hq, p.B, &place, tiles);
-    if (b < 0) return;
-    const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
-    const int nq = qr.y - qr.x, nk = kr.y - kr.x, off = nk - nq;
-    const int first_row = (tiles(b) - 1 - static_cast<int>(place)) * PROMPT_ROWS;
-    // steps of 128 keys: what the tile's last row sees
-    int steps[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row0 = first_row + i * PT;
-        const int seen = row0 < nq ? min(row0 + PT, nq) + off : 0;
-        steps[i] = seen > 0 ? (seen + PT - 1) / PT : 0;
-    }
-    const int all = max(steps[0], steps[1]);
-
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + 2 * Shape::TILE_BYTES;
-    PromptBarriers *bars = reinterpret_cast<PromptBarriers *>(ring + STAGES * Shape::TILE_BYTES);
+    uint8_t *out = ring + STAGES * Shape::TILE_BYTES;
+    PromptBarriers *bars = reinterpret_cast<PromptBarriers *>(out + 8 * OUT_BYTES);
     volatile int *abort = &bars->abort;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
         }
-        mbar_init(&bars->q_full, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->q_full[i], 1);
+            mbar_init(&bars->q_empty[i], 1);
             mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_ready[i], 4);
+            mbar_init(&bars->p_ready[i][0], 4);
+            mbar_init(&bars->p_ready[i][1], 4);
             mbar_init(&bars->o_full[i], 1);
-            mbar_init(&bars->scan[i], 4);
-            bars->dirty_step[i] = bars->skip_step[i] = -1;
+            mbar_init(&bars->o_empty[i], 4);
+            for (int c = 0; c < kCuts; ++c) {
+                mbar_init(&bars->asked[i][c], 1);
+                mbar_init(&bars->scan[i][c], 1);
+            }
+            mbar_init(&bars->work_full[i], 1);
+            mbar_init(&bars->work_empty[i], 11);               // 8 softmax warps, producer, MMA issuer, scanner
+            bars->skip[i] = -1;
         }
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&map_q);
+        tma_prefetch_map(&map_k);
+        tma_prefetch_map(&map_v);
     }
     if (warp == 9) {
         tmem_alloc(&bars->tmem_base, PROMPT_TMEM);
@@ -171,274 +265,360 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bars->tmem_base, 0);
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0 && all > 0) {
-            const int nt = steps[1] > 0 ? 2 : 1;
-            mbar_arrive_expect_tx(&bars->q_full, nt * Shape::TILE_BYTES);
-            for (int i = 0; i < nt; ++i)
-                for (int c = 0; c < Shape::CHUNKS; ++c)
-                    tma_load_2d(smem + i * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, &map_q, &bars->q_full,
-                                head * D + 64 * c, qr.x + first_row + i * PT);
-            const int x = (head / p.G) * D;
-            int issued = 0;
-            for (; issued < 2 * all; ++issued) {             // K_0, V_0, K_1, V_1, ...
-                const int s = issued % STAGES;
-                if (issued >= STAGES && !mbar_wait(&bars->empty[s], (issued / STAGES - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT))
-                    break;
-                mbar_arrive_expect_tx(&bars->full[s], Shape::TILE_BYTES);
-                for (int c = 0; c < Shape::CHUNKS; ++c)
-                    tma_load_2d(ring + s * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, (issued & 1) ? &map_v : &map_k,
-                                &bars->full[s], x + 64 * c, kr.x + (issued >> 1) * PT);
+    // the next piece of work, for every lane of a warp; false when there is none or the CTA gives up
+    auto take = [&](int n, PromptWork *w) {
+        if (!warp_wait(&bars->work_full[n & 1], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) return false;
+        *w = bars->work[n & 1];
+        return w->steps[0] >= 0;
+    };
+    auto give_back = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->work_empty[n & 1]);
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+        if (warp == 11) {
+            // -------------------------------------------------------- the work, this CTA's share of it:
+            // the longest tiles of a sequence first; neighbouring CTAs are the heads of one
+            // tile, which share keys and values
+            auto tiles = [&](int s) {
+                const int2 r = kv::row_range(p.cu_q, s, p.N);
+                return (r.y - r.x + PROMPT_ROWS - 1) / PROMPT_ROWS;
+            };
+            for (int n = 0;; ++n) {
+                const long long item = blockIdx.x + static_cast<long long>(n) * gridDim.x;
+                long long place = 0;
+                const int b = kv::find_item(item / p.Hq, p.B, &place, tiles);
+                PromptWork w{};
+                w.steps[0] = -1;
+                if (b >= 0) {
+                    const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
+                    const int nq = qr.y - qr.x, off = kr.y - kr.x - nq;
+                    const int first = (tiles(b) - 1 - static_cast<int>(place)) * PROMPT_ROWS;
+                    w.row = qr.x + first;
+                    w.rows = nq - first;
+                    w.key = kr.x;
+                    w.head = static_cast<int>(item % p.Hq);
+                    w.seen = first + off;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        // what the tile's last row sees
+                        const int keys = i * PT < w.rows ? min((i + 1) * PT, w.rows) + w.seen : 0;
+                        w.steps[i] = keys > 0 ? (keys + PT - 1) / PT : 0;
+                    }
+                }
+                if (n >= 2 && !warp_wait(&bars->work_empty[n & 1], ((n >> 1) - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) break;
+                if (lane == 0) {
+                    bars->work[n & 1] = w;
+                    mbar_arrive(&bars->work_full[n & 1]);
+                }
+                if (b < 0) break;
             }
-            if (issued < 2 * all) {
+        } else if (warp == 10) {
+            // -------------------------------------------------------- infinities and NaN in V of the steps that a mask cuts
+            int tile = 0;                                    // tiles of the ring so far
+            PromptWork w;
+            for (int n = 0; take(n, &w); ++n) {
+                const int all = max(w.steps[0], w.steps[1]), cut = first_cut(w.seen);
+                bool ok = true;
+                for (int c = 0; ok && c < kCuts; ++c) {
+                    bool bad = false;
+                    // This warp does not follow the ring's turns, and a parity cannot tell a
+                    // turn from the one two before: once the producer has asked for this one,
+                    // it is the one that full[] completes next.
+                    ok = warp_wait(&bars->asked[n & 1][c], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    if (ok && cut + c < all) {
+                        const int k = tile + 2 * (cut + c) + 1;
+                        ok = warp_wait(&bars->full[k % STAGES], (k / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                        const uint4 *v = reinterpret_cast<const uint4 *>(ring + k % STAGES * Shape::TILE_BYTES) + lane;
+#pragma unroll 8
+                        for (int e = 0; e < Shape::TILE_BYTES / 512; ++e) bad |= not_finite(v[e * 32]);
+                    }
+                    bad = __any_sync(0xFFFFFFFFu, bad);
+                    if (lane == 0) {
+                        bars->dirty[n & 1][c] = bad;
+                        mbar_arrive(&bars->scan[n & 1][c]);
+                    }
+                }
+                if (!ok) break;
+                tile += 2 * all;
+                give_back(n);
+            }
+        } else if (warp == 8) {
+            // -------------------------------------------------------- producer
+            int tile = 0;
+            bool ok = true;
+            int q_loaded[2] = {-1, -1};                      // the last work whose queries were asked for
+            PromptWork w;
+            int n = 0;
+            for (; ok && take(n, &w); ++n) {
+                const int all = max(w.steps[0], w.steps[1]), x = (w.head / p.G) * D, cut = first_cut(w.seen);
+                auto load_kv = [&](int k) {                  // K_0, V_0, K_1, V_1, ...
+                    const int s = (tile + k) % STAGES, turn = (tile + k) / STAGES;
+                    ok = ok && (turn == 0 || warp_wait(&bars->empty[s], (turn - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT));
+                    if (!ok) return;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars->full[s], Shape::TILE_BYTES);
+                        for (int c = 0; c < Shape::CHUNKS; ++c)
+                            tma_load_2d(ring + s * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, (k & 1) ? &map_v : &map_k,
+                                        &bars->full[s], x + 64 * c, w.key + (k >> 1) * PT);
+                        if ((k & 1) && (k >> 1) >= cut) mbar_arrive(&bars->asked[n & 1][(k >> 1) - cut]);
+                    }
+                    __syncwarp();
+                };
+                int k = 0;
+                for (; ok && k < 2 && k < 2 * all; ++k) load_kv(k);
+                for (int i = 0; ok && i < 2; ++i) {
+                    ok = n == 0 || warp_wait(&bars->q_empty[i], (n - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars->q_full[i], w.steps[i] > 0 ? Shape::TILE_BYTES : 0);
+                        for (int c = 0; w.steps[i] > 0 && c < Shape::CHUNKS; ++c)
+                            tma_load_2d(smem + i * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, &map_q, &bars->q_full[i],
+                                        w.head * D + 64 * c, w.row + i * PT);
+                    }
+                    q_loaded[i] = n;
+                    __syncwarp();
+                }
+                for (; ok && k < 2 * all; ++k) load_kv(k);
+                tile += k;                                   // (what was asked for, when giving up)
+                if (ok && lane == 0)
+                    for (int c = max(0, all - cut); c < kCuts; ++c) mbar_arrive(&bars->asked[n & 1][c]);      // no such step
+                if (ok) give_back(n);
+            }
+            if (*abort && lane == 0) {
                 // given up: let the loads in flight land before the CTA leaves
                 volatile int never = 0;
-                mbar_wait(&bars->q_full, 0, &never, 0);
-                for (int k = max(0, issued - STAGES); k < issued; ++k)
+                for (int i = 0; i < 2; ++i)
+                    if (q_loaded[i] >= 0) mbar_wait(&bars->q_full[i], q_loaded[i] & 1, &never, 0);
+                for (int k = max(0, tile - STAGES); k < tile; ++k)
                     mbar_wait(&bars->full[k % STAGES], (k / STAGES) & 1, &never, 0);
             }
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && all > 0) {
+        } else {
+            // -------------------------------------------------------- MMA issuer
             const uint32_t id_s = idesc_f16(PT, PT, false, false) | p.negate;
             const uint32_t id_o = idesc_f16(PT, D, false, true);
-            int got = -1;                                    // last ring tile known to have landed
+            const uint32_t q_base = desc_low(smem_u32(smem), 16), ring_base = smem_u32(ring);
+            int tile = 0, got = -1;                          // tiles of the ring before this work; the last known to have landed
+            int done[2] = {0, 0};                            // steps of each tile before this work
+            bool ok = true;
             auto landed = [&](int k) {
-                for (; got < k; ++got)
-                    if (!mbar_wait(&bars->full[(got + 1) % STAGES], ((got + 1) / STAGES) & 1, abort,
-                                   I8R_DEV_PIPELINE_TIMEOUT))
+                for (; got < tile + k; ++got)
+                    if (!warp_wait(&bars->full[(got + 1) % STAGES], ((got + 1) / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT))
                         return false;
                 tc_fence_after_sync();
                 return true;
             };
             auto scores = [&](int i, int j) {
-                const uint32_t a = smem_u32(smem + i * Shape::TILE_BYTES);
-                const uint32_t k = smem_u32(ring + (2 * j) % STAGES * Shape::TILE_BYTES);
+                const uint32_t a = q_base + i * (Shape::TILE_BYTES >> 4);
+                const uint32_t k = desc_low(ring_base + (tile + 2 * j) % STAGES * Shape::TILE_BYTES, 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * Shape::CHUNK_BYTES + (kk & 3) * 32;
-                    mma_f16(tmem + i * PT, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(k + o, 16, 1024), id_s, kk != 0);
+                    const uint32_t o = ((kk >> 2) * Shape::CHUNK_BYTES + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + i * PT, a + o, k + o, id_s, kk != 0);
                 }
-                mma_commit(&bars->s_full[i]);
+                commit_elected(&bars->s_full[i]);
             };
-            bool ok = mbar_wait(&bars->q_full, 0, abort, I8R_DEV_PIPELINE_TIMEOUT) && landed(0);
-            if (ok) {
-                for (int i = 0; i < 2; ++i)
-                    if (steps[i] > 0) scores(i, 0);
-                mma_commit(&bars->empty[0]);
-            }
-            for (int j = 0; ok && j < all; ++j) {
-                for (int i = 0; ok && i < 2; ++i) {
-                    if (j >= steps[i]) continue;
-                    ok = mbar_wait(&bars->p_ready[i], j & 1, abort, I8R_DEV_TMEM_TIMEOUT) && landed(2 * j + 1);
-                    if (!ok) break;
-                    if (*static_cast<volatile int *>(&bars->skip_step[i]) != j) {
-                        const uint32_t v = smem_u32(ring + (2 * j + 1) % STAGES * Shape::TILE_BYTES);
+            PromptWork w;
+            for (int n = 0; ok && take(n, &w); ++n) {
+                const int steps[2] = {__shfl_sync(0xFFFFFFFFu, w.steps[0], 0), __shfl_sync(0xFFFFFFFFu, w.steps[1], 0)};
+                const int all = max(steps[0], steps[1]);
+                give_back(n);
 #pragma unroll
-                        for (int kk = 0; kk < PT / 16; ++kk)
-                            mma_f16_tmem_a(tmem + 2 * PT + i * D, tmem + i * PT + kk * 8,
-                                           smem_desc_sw128(v + kk * 16 * 128, Shape::CHUNK_BYTES, 1024), id_o,
-                                           (j | kk) != 0);
-                    }
-                    if (j + 1 == steps[i]) {
-                        mma_commit(&bars->o_full[i]);
-                    } else {
-                        ok = landed(2 * j + 2);
-                        if (ok) scores(i, j + 1);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    ok = ok && warp_wait(&bars->q_full[i], n & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    if (ok && steps[i] > 0 && (ok = landed(0))) scores(i, 0);
+                    if (ok && steps[i] <= 1) commit_elected(&bars->q_empty[i]);
                 }
-                if (!ok) break;
-                mma_commit(&bars->empty[(2 * j + 1) % STAGES]);
-                if (j + 1 < all) mma_commit(&bars->empty[(2 * j + 2) % STAGES]);
+                if (ok && all > 0) commit_elected(&bars->empty[tile % STAGES]);
+                for (int i = 0; i < 2; ++i)
+                    if (ok && steps[i] == 0) {               // a tile without keys
+                        ok = n == 0 || warp_wait(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                        if (ok) commit_elected(&bars->o_full[i]);
+                    }
+                for (int j = 0; ok && j < all; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || j >= steps[i]) continue;
+                        // the sums are free once the work before has been read out of them
+                        if (j == 0 && n > 0) ok = warp_wait(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                        // the first 64 keys' P while the softmax warps are at the other 64
+                        const uint32_t v = desc_low(ring_base + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, Shape::CHUNK_BYTES);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            ok = ok && warp_wait(&bars->p_ready[i][half], (done[i] + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT) &&
+                                 landed(2 * j + 1);
+                            if (!ok || *static_cast<volatile int *>(&bars->skip[i]) == done[i] + j) continue;
+#pragma unroll
+                            for (int kk = half * PT / 32; kk < (half + 1) * PT / 32; ++kk)
+                                mma_ts(tmem + 2 * PT + i * D, tmem + i * PT + kk * 8, v + (kk * 16 * 128 >> 4), id_o, (j | kk) != 0);
+                        }
+                        if (!ok) continue;
+                        if (j + 1 == steps[i]) {
+                            commit_elected(&bars->o_full[i]);
+                        } else {
+                            ok = landed(2 * j + 2);
+                            if (ok) scores(i, j + 1);
+                            if (ok && j + 2 == steps[i]) commit_elected(&bars->q_empty[i]);      // its last scores
+                        }
+                    }
+                    if (!ok) break;
+                    commit_elected(&bars->empty[(tile + 2 * j + 1) % STAGES]);
+                    if (j + 1 < all) commit_elected(&bars->empty[(tile + 2 * j + 2) % STAGES]);
+                }
+                tile += 2 * all;
+                done[0] += steps[0];
+                done[1] += steps[1];
             }
             volatile int never = 0;
-            mma_commit(&bars->drain);
-            mbar_wait(&bars->drain, 0, &never, 0);
+            commit_elected(&bars->drain);
+            if (lane == 0) mbar_wait(&bars->drain, 0, &never, 0);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax, one row a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
         const int i = warp >> 2, quad = warp & 3;
-        const int n = steps[i];
-        const int row = first_row + i * PT + quad * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lanes + i * PT, t_o = tmem + lanes + 2 * PT + i * D;
-        const int lim = row + off;                              // the last key the row sees
         const float sl2 = p.scale_log2, raise = RAISE / sl2;
-        float m = -INFINITY, l = 0.0f;
-        uint32_t scans = 0;
+        int tile = 0, done = 0;                                 // tiles of the ring, steps of this tile before this work
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = warp_wait(&bars->s_full[i], j & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-            if (!ok) break;
-            tc_fence_after_sync();
-            // a step that every row of the tile sees whole needs no mask
-            const bool cut = j * PT + PT - 1 > first_row + i * PT + off;
-            const int seen = lim - j * PT;                      // columns 0 .. seen stay
-            // The scores are read twice (tensor memory's bandwidth is idle
-            // otherwise), so that half of them are in registers at a time.
-            float x[2][32];
-            auto fetch = [&](int h) {
-                uint32_t r[2][32];
-                tmem_ld32(t_s + 64 * h, r[0]);
-                tmem_ld32(t_s + 64 * h + 32, r[1]);
+        PromptWork w;
+        for (int n = 0; ok && take(n, &w); ++n) {
+            const int steps = w.steps[i], cut0 = first_cut(w.seen), cut = first_cut(w.seen + i * PT);
+            const int lim = w.seen + i * PT + quad * 32 + lane; // the last key the row sees
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < steps; ++j) {
+                ok = warp_wait(&bars->s_full[i], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t r[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r[c]);
                 tmem_wait_ld();
+                // a step that every row of the tile sees whole needs no mask
+                bool dirty = false;
+                if (j >= cut) {
+                    const int seen = lim - j * PT;              // columns 0 .. seen stay
 #pragma unroll
-                for (int e = 0; e < 64; ++e) x[e >> 5][e & 31] = __uint_as_float(r[e >> 5][e & 31]);
-                if (cut) {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        x[e >> 5][e & 31] = 64 * h + e <= seen ? x[e >> 5][e & 31] : -INFINITY;
+                    for (int e = 0; e < PT; ++e)
+                        if (e > seen) r[e >> 5][e & 31] = 0xFF800000u;  // -infinity
+                    ok = warp_wait(&bars->scan[n & 1][j - cut0], (n >> 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                    if (!ok) break;
+                    dirty = *static_cast<volatile int *>(&bars->dirty[n & 1][j - cut0]) != 0;
+                    if (dirty && lane == 0) *static_cast<volatile int *>(&bars->skip[i]) = done + j;
                 }
-            };
-            float mx = -INFINITY;
+                auto x = [&](int e) { return __uint_as_float(r[e >> 5][e & 31]); };
+                float top[4] = {x(0), x(1), x(2), x(3)};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                fetch(h);
-                float top[4] = {mx, x[0][0], x[0][1], x[0][2]};
+                for (int e = 4; e < PT - 4; e += 8)
 #pragma unroll
-                for (int e = 3; e < 63; e += 2)
-                    top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], x[e >> 5][e & 31], x[(e + 1) >> 5][(e + 1) & 31]);
-                mx = fmaxf(max3(top[0], top[1], top[2]), fmaxf(top[3], x[1][31]));
-            }
-            if (__any_sync(0xFFFFFFFFu, mx > m + raise)) {
-                const float to = fmaxf(m, mx);
-                const float alpha = m == -INFINITY ? 0.0f : ex2((m - to) * sl2);
-                l *= alpha;
-                m = to;
-                if (j > 0) {
+                    for (int c = 0; c < 4; ++c) top[c] = max3(top[c], x(e + 2 * c), x(e + 2 * c + 1));
+                const float mx = fmaxf(max3(max3(top[0], top[1], x(PT - 4)), max3(top[2], top[3], x(PT - 3)), x(PT - 2)), x(PT - 1));
+                if (__any_sync(0xFFFFFFFFu, mx > m + raise)) {
+                    const float to = fmaxf(m, mx);
+                    const float alpha = m == -INFINITY ? 0.0f : ex2((m - to) * sl2);
+                    l *= alpha;
+                    m = to;
+                    if (j > 0) {
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + 32 * c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(t_o + 32 * c, o);
-                    }
-                }
-            }
-            // p = 2^(x * scale_log2 - m * scale_log2); a row that has seen nothing yet has all -inf
-            const float ref = m == -INFINITY ? 0.0f : -m * sl2;
-            const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(ref, ref);
-            uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                fetch(h);
-                uint32_t out[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 y = unpack2(fma2(pack2(x[e >> 4][2 * (e & 15)], x[e >> 4][2 * (e & 15) + 1]), sl22, ref2));
-                    const float p0 = ex2(y.x), p1 = ex2(y.y);
-                    sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
-                    const __half2 h2 = __floats2half2_rn(p0, p1);
-                    out[e] = *reinterpret_cast<const uint32_t *>(&h2);
-                }
-                tmem_st32(t_s + 32 * h, out);
-            }
-            const float2 s2 = unpack2(add2(sum[0], sum[1]));
-            l += s2.x + s2.y;
-            tmem_wait_st();
-            if (cut) {
-                // V's rows of a step that a mask cuts: this warp looks at 32 of them
-                const int k = 2 * j + 1;
-                uint8_t *v = ring + k % STAGES * Shape::TILE_BYTES;
-                ok = warp_wait(&bars->full[k % STAGES], (k / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
-                if (!ok) break;
-                bool bad = false;
-#pragma unroll
-                for (int c = 0; c < Shape::CHUNKS; ++c)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        bad |= not_finite(*reinterpret_cast<const uint4 *>(v + c * Shape::CHUNK_BYTES + quad * 4096 +
-                                                                           e * 512 + lane * 16));
-                if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) *static_cast<volatile int *>(&bars->dirty_step[i]) = j;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->scan[i]);
-                ok = warp_wait(&bars->scan[i], scans & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                if (!ok) break;
-                ++scans;
-                if (*static_cast<volatile int *>(&bars->dirty_step[i]) == j) {
-                    // P V over the keys that the row sees
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                        if (j > 0) {
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
                             tmem_ld32(t_o + 32 * c, o);
                             tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(t_o + 32 * c, o);
                         }
-#pragma unroll 1
-                        for (int kk = 0; kk < PT; kk += 2) {
-                            uint32_t pp;
-                            tmem_ld1(t_s + kk / 2, pp);
-                            tmem_wait_ld();
-                            const float2 pf = __half22float2(*reinterpret_cast<const __half2 *>(&pp));
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                if (j * PT + kk + z > lim) continue;
-                                const float pz = z ? pf.y : pf.x;
-                                const uint8_t *src = v + (c >> 1) * Shape::CHUNK_BYTES + (kk + z) * 128;
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const uint4 q = *reinterpret_cast<const uint4 *>(src + (((4 * (c & 1) + u) ^ ((kk + z) & 7)) << 4));
-                                    const __half2 *hv = reinterpret_cast<const __half2 *>(&q);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float2 f = __half22float2(hv[e]);
-                                        uint32_t &o0 = o[8 * u + 2 * e], &o1 = o[8 * u + 2 * e + 1];
-                                        o0 = __float_as_uint(fmaf(pz, f.x, __uint_as_float(o0)));
-                                        o1 = __float_as_uint(fmaf(pz, f.y, __uint_as_float(o1)));
-                                    }
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        tmem_st32(t_o + 32 * c, o);
                     }
-                    tmem_wait_st();
-                    if (lane == 0) *static_cast<volatile int *>(&bars->skip_step[i]) = j;
                 }
+                // p = 2^(x * scale_log2 - m * scale_log2); a row that has seen nothing yet has all -inf
+                const float ref = m == -INFINITY ? 0.0f : -m * sl2;
+                const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(ref, ref);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t out[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = unpack2(fma2(pack2(x(32 * c + 2 * e), x(32 * c + 2 * e + 1)), sl22, ref2));
+                        const float p0 = ex2(y.x), p1 = ex2(y.y);
+                        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+                        const __half2 h2 = __floats2half2_rn(p0, p1);
+                        out[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                    }
+                    tmem_st16(t_s + 16 * c, out);
+                    if (c == 1) {
+                        tmem_wait_st();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
+                    }
+                }
+                const float2 s2 = unpack2(add2(sum[0], sum[1]));
+                l += s2.x + s2.y;
+                tmem_wait_st();
+                if (dirty)
+                    values_seen<D>(t_s, t_o, ring + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, j > 0, lim - j * PT);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_ready[i][1]);
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_ready[i]);
-        }
-        if (ok && n > 0) {
-            ok = warp_wait(&bars->o_full[i], 0, abort, I8R_DEV_TMEM_TIMEOUT);
+            ok = ok && warp_wait(&bars->o_full[i], n & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+            if (!ok) break;
             tc_fence_after_sync();
-        }
-        if (ok) {
+            // O / l in fp16, 64 columns at a time through shared memory (piece e, 16 bytes, of
+            // row r in place e ^ (r % 8)), so that whole lines are written.  A row that sees no
+            // key is zeros, whatever its tile's steps left.
+            const bool none = steps == 0 || lim < 0;            // (then what tensor memory holds is not looked at)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            __half *dst = p.O + static_cast<size_t>(qr.x + row) * p.ldo + static_cast<size_t>(head) * D;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(t_o + 32 * c, o);
+            uint8_t *mine = out + warp * OUT_BYTES;
+            const int first = i * PT + quad * 32;
+            __half *dst = p.O + static_cast<size_t>(w.row + first + (lane >> 3)) * p.ldo + static_cast<size_t>(w.head) * D +
+                          8 * (lane & 7);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + 64 * h + 32 * z, o);
                     tmem_wait_ld();
-                } else {
+                    if (z == 1 && h + 1 == D / 64) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->o_empty[i]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-                uint4 out[4];
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 v;
+                        uint32_t *f = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const __half2 h2 = __floats2half2_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    reinterpret_cast<uint32_t *>(out)[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 h2 = __floats2half2_rn(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                                 __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                            f[k] = *reinterpret_cast<const uint32_t *>(&h2);
+                        }
+                        if (none) v = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(mine + lane * 128 + (((4 * z + e) ^ (lane & 7)) << 4)) = v;
+                    }
                 }
-                // a row that sees no key: zeros, whatever its tile's steps left
-                if (lim < 0) out[0] = out[1] = out[2] = out[3] = make_uint4(0u, 0u, 0u, 0u);
-                if (row < nq) {
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * e) = out[e];
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 4 * k + (lane >> 3);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                    if (first + row < w.rows)
+                        *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(4 * k) * p.ldo + 64 * h) = v;
                 }
+                __syncwarp();
             }
+            tile += 2 * max(w.steps[0], w.steps[1]);
+            done += steps;
+            give_back(n);
         }
     }
 

@@ -1391,7 +1391,7 @@ i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, lo
     // leaves every finite score at 0 (infinities, the masked places, stay)
     p.scale_log2 = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
     p.negate = scale < 0.0f ? 1u << 13 : 0u;
-    const dim3 grid(static_cast<unsigned>(tiles * Hq));
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(tiles * Hq, dev->sms)));      // one CTA an SM
     if (D == 128)
         attn::attention_prompt_kernel<128><<<grid, attn::PROMPT_THREADS, attn::PromptShape<128>::SMEM, stream>>>(
             map_q, map_k, map_v, p);
