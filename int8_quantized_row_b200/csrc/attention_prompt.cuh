@@ -161,14 +161,10 @@ __device__ __forceinline__ void commit_elected(uint64_t *bar) {
         : "memory");
 }
 
-// Whether any of eight fp16 values is an infinity or NaN (exponent all ones).
-__device__ __forceinline__ bool not_finite(const uint4 &v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        bad |= (w[i] & 0x7C007C00u) >= 0x7C000000u || (w[i] & 0x00007C00u) == 0x00007C00u;
-    return bad;
+// A wait of a whole warp that is usually over already: all lanes look once (about 40
+// cycles; lane 0's look and its broadcast take 240), and only then lane 0 waits.
+__device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity, volatile int *abort, int code) {
+    return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, abort, code);
 }
 
 // P V of one step over the keys that each row sees, without the tensor cores: O (in
@@ -269,7 +265,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 
     // the next piece of work, for every lane of a warp; false when there is none or the CTA gives up
     auto take = [&](int n, PromptWork *w) {
-        if (!warp_wait(&bars->work_full[n & 1], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) return false;
+        if (!ready(&bars->work_full[n & 1], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) return false;
         *w = bars->work[n & 1];
         return w->steps[0] >= 0;
     };
@@ -325,19 +321,22 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 const int all = max(w.steps[0], w.steps[1]), cut = first_cut(w.seen);
                 bool ok = true;
                 for (int c = 0; ok && c < kCuts; ++c) {
-                    bool bad = false;
                     // This warp does not follow the ring's turns, and a parity cannot tell a
                     // turn from the one two before: once the producer has asked for this one,
                     // it is the one that full[] completes next.
-                    ok = warp_wait(&bars->asked[n & 1][c], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    ok = ready(&bars->asked[n & 1][c], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    uint32_t top[4] = {0u, 0u, 0u, 0u};      // largest magnitudes, as bits
                     if (ok && cut + c < all) {
                         const int k = tile + 2 * (cut + c) + 1;
-                        ok = warp_wait(&bars->full[k % STAGES], (k / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                        ok = ready(&bars->full[k % STAGES], (k / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
                         const uint4 *v = reinterpret_cast<const uint4 *>(ring + k % STAGES * Shape::TILE_BYTES) + lane;
-#pragma unroll 8
-                        for (int e = 0; e < Shape::TILE_BYTES / 512; ++e) bad |= not_finite(v[e * 32]);
+#pragma unroll 4
+                        for (int e = 0; e < Shape::TILE_BYTES / 512; e += 4)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) top[z] = kv::max_bits(v[(e + z) * 32], top[z]);
                     }
-                    bad = __any_sync(0xFFFFFFFFu, bad);
+                    const uint32_t m = __vmaxu2(__vmaxu2(top[0], top[1]), __vmaxu2(top[2], top[3]));
+                    const bool bad = __any_sync(0xFFFFFFFFu, (m >> 16) >= 0x7C00u || (m & 0xFFFFu) >= 0x7C00u);
                     if (lane == 0) {
                         bars->dirty[n & 1][c] = bad;
                         mbar_arrive(&bars->scan[n & 1][c]);
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 const int all = max(w.steps[0], w.steps[1]), x = (w.head / p.G) * D, cut = first_cut(w.seen);
                 auto load_kv = [&](int k) {                  // K_0, V_0, K_1, V_1, ...
                     const int s = (tile + k) % STAGES, turn = (tile + k) / STAGES;
-                    ok = ok && (turn == 0 || warp_wait(&bars->empty[s], (turn - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT));
+                    ok = ok && (turn == 0 || ready(&bars->empty[s], (turn - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT));
                     if (!ok) return;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars->full[s], Shape::TILE_BYTES);
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 int k = 0;
                 for (; ok && k < 2 && k < 2 * all; ++k) load_kv(k);
                 for (int i = 0; ok && i < 2; ++i) {
-                    ok = n == 0 || warp_wait(&bars->q_empty[i], (n - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    ok = n == 0 || ready(&bars->q_empty[i], (n - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars->q_full[i], w.steps[i] > 0 ? Shape::TILE_BYTES : 0);
@@ -402,19 +401,16 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             const uint32_t id_s = idesc_f16(PT, PT, false, false) | p.negate;
             const uint32_t id_o = idesc_f16(PT, D, false, true);
             const uint32_t q_base = desc_low(smem_u32(smem), 16), ring_base = smem_u32(ring);
-            int tile = 0, got = -1;                          // tiles of the ring before this work; the last known to have landed
+            int tile = 0;                                    // tiles of the ring before this work
             int done[2] = {0, 0};                            // steps of each tile before this work
             bool ok = true;
-            auto landed = [&](int k) {
-                for (; got < tile + k; ++got)
-                    if (!warp_wait(&bars->full[(got + 1) % STAGES], ((got + 1) / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT))
-                        return false;
-                tc_fence_after_sync();
-                return true;
+            auto landed = [&](int k) {                       // each of the ring's tiles, in order
+                return ready(&bars->full[(tile + k) % STAGES], ((tile + k) / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
             };
             auto scores = [&](int i, int j) {
                 const uint32_t a = q_base + i * (Shape::TILE_BYTES >> 4);
                 const uint32_t k = desc_low(ring_base + (tile + 2 * j) % STAGES * Shape::TILE_BYTES, 16);
+                tc_fence_after_sync();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * Shape::CHUNK_BYTES + (kk & 3) * 32) >> 4;
@@ -425,33 +421,36 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             PromptWork w;
             for (int n = 0; ok && take(n, &w); ++n) {
                 const int steps[2] = {__shfl_sync(0xFFFFFFFFu, w.steps[0], 0), __shfl_sync(0xFFFFFFFFu, w.steps[1], 0)};
-                const int all = max(steps[0], steps[1]);
+                const int all = max(steps[0], steps[1]), cut = first_cut(w.seen);
                 give_back(n);
+                if (all > 0) ok = landed(0);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    ok = ok && warp_wait(&bars->q_full[i], n & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
-                    if (ok && steps[i] > 0 && (ok = landed(0))) scores(i, 0);
+                    ok = ok && ready(&bars->q_full[i], n & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    if (ok && steps[i] > 0) scores(i, 0);
                     if (ok && steps[i] <= 1) commit_elected(&bars->q_empty[i]);
                 }
                 if (ok && all > 0) commit_elected(&bars->empty[tile % STAGES]);
                 for (int i = 0; i < 2; ++i)
                     if (ok && steps[i] == 0) {               // a tile without keys
-                        ok = n == 0 || warp_wait(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                        ok = n == 0 || ready(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                         if (ok) commit_elected(&bars->o_full[i]);
                     }
                 for (int j = 0; ok && j < all; ++j) {
+                    bool have_v = false, have_k = false;     // this step's V, the next one's K
+                    const uint32_t v = desc_low(ring_base + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, Shape::CHUNK_BYTES);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         if (!ok || j >= steps[i]) continue;
                         // the sums are free once the work before has been read out of them
-                        if (j == 0 && n > 0) ok = warp_wait(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                        if (j == 0 && n > 0) ok = ready(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                         // the first 64 keys' P while the softmax warps are at the other 64
-                        const uint32_t v = desc_low(ring_base + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, Shape::CHUNK_BYTES);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            ok = ok && warp_wait(&bars->p_ready[i][half], (done[i] + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT) &&
-                                 landed(2 * j + 1);
-                            if (!ok || *static_cast<volatile int *>(&bars->skip[i]) == done[i] + j) continue;
+                            ok = ok && ready(&bars->p_ready[i][half], (done[i] + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                            if (!have_v) ok = ok && (have_v = landed(2 * j + 1));
+                            if (!ok || (j >= cut && *static_cast<volatile int *>(&bars->skip[i]) == done[i] + j)) continue;
+                            tc_fence_after_sync();
 #pragma unroll
                             for (int kk = half * PT / 32; kk < (half + 1) * PT / 32; ++kk)
                                 mma_ts(tmem + 2 * PT + i * D, tmem + i * PT + kk * 8, v + (kk * 16 * 128 >> 4), id_o, (j | kk) != 0);
@@ -460,7 +459,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         if (j + 1 == steps[i]) {
                             commit_elected(&bars->o_full[i]);
                         } else {
-                            ok = landed(2 * j + 2);
+                            if (!have_k) ok = have_k = landed(2 * j + 2);
                             if (ok) scores(i, j + 1);
                             if (ok && j + 2 == steps[i]) commit_elected(&bars->q_empty[i]);      // its last scores
                         }
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             const int lim = w.seen + i * PT + quad * 32 + lane; // the last key the row sees
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
-                ok = warp_wait(&bars->s_full[i], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                ok = ready(&bars->s_full[i], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t r[4][32];
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < PT; ++e)
                         if (e > seen) r[e >> 5][e & 31] = 0xFF800000u;  // -infinity
-                    ok = warp_wait(&bars->scan[n & 1][j - cut0], (n >> 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                    ok = ready(&bars->scan[n & 1][j - cut0], (n >> 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                     if (!ok) break;
                     dirty = *static_cast<volatile int *>(&bars->dirty[n & 1][j - cut0]) != 0;
                     if (dirty && lane == 0) *static_cast<volatile int *>(&bars->skip[i]) = done + j;
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_ready[i][1]);
             }
-            ok = ok && warp_wait(&bars->o_full[i], n & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+            ok = ok && ready(&bars->o_full[i], n & 1, abort, I8R_DEV_TMEM_TIMEOUT);
             if (!ok) break;
             tc_fence_after_sync();
             // O / l in fp16, 64 columns at a time through shared memory (piece e, 16 bytes, of
