@@ -29,10 +29,10 @@
 // CTAs are persistent and everything crosses from one 256-row piece of work to the
 // next: the next Q, K and V are loaded and its first scores computed while the last
 // one's sums are scaled and stored.  Roles: warps 0-3 and 4-7 the two tiles' softmax,
-// 8 the TMA producer, 9 the MMA issuer (the whole warp in step, so that operands stay
-// in uniform registers; with one lane in a branch an MMA took 140 cycles to issue, of
-// the 64 it runs), 10 looks over V for what a mask must hide, 11 finds the work.
-// Every wait is bounded (timeout -> device status word).
+// 8 the TMA producer, 9 and 10 the tiles' MMA issuers (a whole warp in step, so that
+// operands stay in uniform registers; one warp for both tiles needed about 2000
+// cycles for a tile's step of 1024), 11 finds the work and looks over V for what a
+// mask must hide.  Every wait is bounded (timeout -> device status word).
 #pragma once
 
 #include "attention_decode.cuh"
@@ -60,7 +60,7 @@ struct PromptShape {
     static constexpr int CHUNK_BYTES = PT * 128;
     static constexpr int TILE_BYTES = CHUNKS * CHUNK_BYTES;    // a Q, K or V tile
     static constexpr int STAGES = D == 128 ? 4 : 10;
-    static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 8 * OUT_BYTES + 512;
+    static constexpr size_t SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 8 * OUT_BYTES + 1024;
 };
 
 struct PromptParams {
@@ -84,22 +84,24 @@ struct PromptWork {
 constexpr int kCuts = 3;
 __device__ __forceinline__ int first_cut(int seen) { return seen + 1 > 0 ? (seen + 1) / PT : 0; }
 
-// Barriers that complete once per piece of work have parity (work & 1); those of the
-// two work slots (work >> 1) & 1.
+constexpr int kWorkSlots = 4;                  // pieces of work known at a time
+// Barriers that complete once per piece of work have parity (work & 1); those of a
+// work slot (work / kWorkSlots) & 1.
 struct PromptBarriers {
     uint64_t full[10], empty[10];              // the K/V ring
     uint64_t q_full[2], q_empty[2];            // a tile's queries
     uint64_t s_full[2], p_ready[2][2];         // scores; P: tile, half of the keys (once per step)
     uint64_t o_full[2], o_empty[2];            // the sums
-    uint64_t asked[2][kCuts], scan[2][kCuts];  // V of a cut step: asked for, looked over (work slot, cut)
-    uint64_t work_full[2], work_empty[2];
-    uint64_t drain;
-    PromptWork work[2];
+    uint64_t turn[2][4];                       // tile i's warp has done its exponentials: the other tile's may begin
+    uint64_t asked[kWorkSlots][kCuts], scan[kWorkSlots][kCuts];      // V of a cut step: asked for, looked over
+    uint64_t work_full[kWorkSlots], work_empty[kWorkSlots];
+    uint64_t drain[2];
+    PromptWork work[kWorkSlots];
     uint32_t tmem_base;
     int abort;
-    int dirty[2][kCuts], skip[2];              // a cut step's V is not finite; the step (counted through) whose P V is done
+    int dirty[kWorkSlots][kCuts], skip[2];     // a cut step's V is not finite; the step (counted through) whose P V is done
 };
-static_assert(sizeof(PromptBarriers) <= 512, "barrier block outgrew its shared-memory reserve");
+static_assert(sizeof(PromptBarriers) <= 1024, "barrier block outgrew its shared-memory reserve");
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -227,7 +229,15 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->empty[s], 2);                     // both tiles' MMAs
+        }
+        for (int s = 0; s < kWorkSlots; ++s) {
+            for (int c = 0; c < kCuts; ++c) {
+                mbar_init(&bars->asked[s][c], 1);
+                mbar_init(&bars->scan[s][c], 1);
+            }
+            mbar_init(&bars->work_full[s], 1);
+            mbar_init(&bars->work_empty[s], 11);               // 8 softmax warps, producer, 2 MMA issuers
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
@@ -237,15 +247,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             mbar_init(&bars->p_ready[i][1], 4);
             mbar_init(&bars->o_full[i], 1);
             mbar_init(&bars->o_empty[i], 4);
-            for (int c = 0; c < kCuts; ++c) {
-                mbar_init(&bars->asked[i][c], 1);
-                mbar_init(&bars->scan[i][c], 1);
-            }
-            mbar_init(&bars->work_full[i], 1);
-            mbar_init(&bars->work_empty[i], 11);               // 8 softmax warps, producer, MMA issuer, scanner
+            for (int k = 0; k < 4; ++k) mbar_init(&bars->turn[i][k], 1);
             bars->skip[i] = -1;
         }
-        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->drain[0], 1);
+        mbar_init(&bars->drain[1], 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -265,13 +271,13 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 
     // the next piece of work, for every lane of a warp; false when there is none or the CTA gives up
     auto take = [&](int n, PromptWork *w) {
-        if (!ready(&bars->work_full[n & 1], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) return false;
-        *w = bars->work[n & 1];
+        if (!ready(&bars->work_full[n % kWorkSlots], (n / kWorkSlots) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) return false;
+        *w = bars->work[n % kWorkSlots];
         return w->steps[0] >= 0;
     };
     auto give_back = [&](int n) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->work_empty[n & 1]);
+        if (lane == 0) mbar_arrive(&bars->work_empty[n % kWorkSlots]);
     };
 
     if (warp >= 8) {
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 const int2 r = kv::row_range(p.cu_q, s, p.N);
                 return (r.y - r.x + PROMPT_ROWS - 1) / PROMPT_ROWS;
             };
-            for (int n = 0;; ++n) {
+            auto publish = [&](int n) {                      // false: there is no more, or the CTA gives up
                 const long long item = blockIdx.x + static_cast<long long>(n) * gridDim.x;
                 long long place = 0;
                 const int b = kv::find_item(item / p.Hq, p.B, &place, tiles);
@@ -306,25 +312,30 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         w.steps[i] = keys > 0 ? (keys + PT - 1) / PT : 0;
                     }
                 }
-                if (n >= 2 && !warp_wait(&bars->work_empty[n & 1], ((n >> 1) - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT)) break;
+                const int slot = n % kWorkSlots;
+                if (n >= kWorkSlots &&
+                    !ready(&bars->work_empty[slot], (n / kWorkSlots - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT))
+                    return false;
                 if (lane == 0) {
-                    bars->work[n & 1] = w;
-                    mbar_arrive(&bars->work_full[n & 1]);
+                    bars->work[slot] = w;
+                    mbar_arrive(&bars->work_full[slot]);
                 }
-                if (b < 0) break;
-            }
-        } else if (warp == 10) {
-            // -------------------------------------------------------- infinities and NaN in V of the steps that a mask cuts
+                __syncwarp();
+                return b >= 0;
+            };
             int tile = 0;                                    // tiles of the ring so far
-            PromptWork w;
-            for (int n = 0; take(n, &w); ++n) {
+            bool more = publish(0), ok = true;
+            for (int n = 0; ok && more; ++n) {
+                more = publish(n + 1);
+                // infinities and NaN in V of the steps that a mask cuts
+                const int slot = n % kWorkSlots, parity = (n / kWorkSlots) & 1;
+                const PromptWork w = bars->work[slot];
                 const int all = max(w.steps[0], w.steps[1]), cut = first_cut(w.seen);
-                bool ok = true;
                 for (int c = 0; ok && c < kCuts; ++c) {
                     // This warp does not follow the ring's turns, and a parity cannot tell a
                     // turn from the one two before: once the producer has asked for this one,
                     // it is the one that full[] completes next.
-                    ok = ready(&bars->asked[n & 1][c], (n >> 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                    ok = ready(&bars->asked[slot][c], parity, abort, I8R_DEV_PIPELINE_TIMEOUT);
                     uint32_t top[4] = {0u, 0u, 0u, 0u};      // largest magnitudes, as bits
                     if (ok && cut + c < all) {
                         const int k = tile + 2 * (cut + c) + 1;
@@ -338,13 +349,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     const uint32_t m = __vmaxu2(__vmaxu2(top[0], top[1]), __vmaxu2(top[2], top[3]));
                     const bool bad = __any_sync(0xFFFFFFFFu, (m >> 16) >= 0x7C00u || (m & 0xFFFFu) >= 0x7C00u);
                     if (lane == 0) {
-                        bars->dirty[n & 1][c] = bad;
-                        mbar_arrive(&bars->scan[n & 1][c]);
+                        bars->dirty[slot][c] = bad;
+                        mbar_arrive(&bars->scan[slot][c]);
                     }
                 }
-                if (!ok) break;
                 tile += 2 * all;
-                give_back(n);
             }
         } else if (warp == 8) {
             // -------------------------------------------------------- producer
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         for (int c = 0; c < Shape::CHUNKS; ++c)
                             tma_load_2d(ring + s * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, (k & 1) ? &map_v : &map_k,
                                         &bars->full[s], x + 64 * c, w.key + (k >> 1) * PT);
-                        if ((k & 1) && (k >> 1) >= cut) mbar_arrive(&bars->asked[n & 1][(k >> 1) - cut]);
+                        if ((k & 1) && (k >> 1) >= cut) mbar_arrive(&bars->asked[n % kWorkSlots][(k >> 1) - cut]);
                     }
                     __syncwarp();
                 };
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 for (; ok && k < 2 * all; ++k) load_kv(k);
                 tile += k;                                   // (what was asked for, when giving up)
                 if (ok && lane == 0)
-                    for (int c = max(0, all - cut); c < kCuts; ++c) mbar_arrive(&bars->asked[n & 1][c]);      // no such step
+                    for (int c = max(0, all - cut); c < kCuts; ++c) mbar_arrive(&bars->asked[n % kWorkSlots][c]);      // no such step
                 if (ok) give_back(n);
             }
             if (*abort && lane == 0) {
@@ -400,81 +409,75 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             // -------------------------------------------------------- MMA issuer
             const uint32_t id_s = idesc_f16(PT, PT, false, false) | p.negate;
             const uint32_t id_o = idesc_f16(PT, D, false, true);
-            const uint32_t q_base = desc_low(smem_u32(smem), 16), ring_base = smem_u32(ring);
-            int tile = 0;                                    // tiles of the ring before this work
-            int done[2] = {0, 0};                            // steps of each tile before this work
+            const int i = warp - 9;                          // the tile
+            const uint32_t q_base = desc_low(smem_u32(smem + i * Shape::TILE_BYTES), 16), ring_base = smem_u32(ring);
+            const uint32_t t_s = tmem + i * PT, t_o = tmem + 2 * PT + i * D;
+            int tile = 0, done = 0;                          // tiles of the ring, steps of this tile before this work
             bool ok = true;
             auto landed = [&](int k) {                       // each of the ring's tiles, in order
                 return ready(&bars->full[(tile + k) % STAGES], ((tile + k) / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
             };
-            auto scores = [&](int i, int j) {
-                const uint32_t a = q_base + i * (Shape::TILE_BYTES >> 4);
+            auto scores = [&](int j) {
                 const uint32_t k = desc_low(ring_base + (tile + 2 * j) % STAGES * Shape::TILE_BYTES, 16);
                 tc_fence_after_sync();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk >> 2) * Shape::CHUNK_BYTES + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + i * PT, a + o, k + o, id_s, kk != 0);
+                    mma_ss(t_s, q_base + o, k + o, id_s, kk != 0);
                 }
                 commit_elected(&bars->s_full[i]);
             };
             PromptWork w;
             for (int n = 0; ok && take(n, &w); ++n) {
-                const int steps[2] = {__shfl_sync(0xFFFFFFFFu, w.steps[0], 0), __shfl_sync(0xFFFFFFFFu, w.steps[1], 0)};
-                const int all = max(steps[0], steps[1]), cut = first_cut(w.seen);
+                const int steps = __shfl_sync(0xFFFFFFFFu, w.steps[i], 0), all = max(w.steps[0], w.steps[1]);
+                const int cut = first_cut(w.seen);
                 give_back(n);
-                if (all > 0) ok = landed(0);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ok = ok && ready(&bars->q_full[i], n & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
-                    if (ok && steps[i] > 0) scores(i, 0);
-                    if (ok && steps[i] <= 1) commit_elected(&bars->q_empty[i]);
+                ok = ready(&bars->q_full[i], n & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
+                if (ok && steps > 0) {
+                    ok = landed(0);
+                    if (ok) scores(0);
                 }
-                if (ok && all > 0) commit_elected(&bars->empty[tile % STAGES]);
-                for (int i = 0; i < 2; ++i)
-                    if (ok && steps[i] == 0) {               // a tile without keys
-                        ok = n == 0 || ready(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                        if (ok) commit_elected(&bars->o_full[i]);
-                    }
+                if (ok && steps <= 1) commit_elected(&bars->q_empty[i]);
+                // the sums are free once the work before has been read out of them
+                ok = ok && (n == 0 || ready(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT));
+                if (ok && steps == 0) commit_elected(&bars->o_full[i]);          // a tile without keys
                 for (int j = 0; ok && j < all; ++j) {
-                    bool have_v = false, have_k = false;     // this step's V, the next one's K
+                    // Both issuers pass every tile of the ring, also those that their own tile has no step
+                    // for (waiting for its turn: a commit must not count for the turn before).
+                    if (j >= steps) {
+                        for (int k = 2 * j; ok && k < 2 * j + 2; ++k)
+                            if ((ok = landed(k))) commit_elected(&bars->empty[(tile + k) % STAGES]);
+                        continue;
+                    }
+                    commit_elected(&bars->empty[(tile + 2 * j) % STAGES]);       // K_j: its scores are issued
                     const uint32_t v = desc_low(ring_base + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, Shape::CHUNK_BYTES);
+                    // the first 64 keys' P while the softmax warps are at the other 64
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok || j >= steps[i]) continue;
-                        // the sums are free once the work before has been read out of them
-                        if (j == 0 && n > 0) ok = ready(&bars->o_empty[i], (n - 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                        // the first 64 keys' P while the softmax warps are at the other 64
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && ready(&bars->p_ready[i][half], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                        if (half == 0) ok = ok && landed(2 * j + 1);
+                        if (!ok || (j >= cut && *static_cast<volatile int *>(&bars->skip[i]) == done + j)) continue;
+                        tc_fence_after_sync();
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            ok = ok && ready(&bars->p_ready[i][half], (done[i] + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                            if (!have_v) ok = ok && (have_v = landed(2 * j + 1));
-                            if (!ok || (j >= cut && *static_cast<volatile int *>(&bars->skip[i]) == done[i] + j)) continue;
-                            tc_fence_after_sync();
-#pragma unroll
-                            for (int kk = half * PT / 32; kk < (half + 1) * PT / 32; ++kk)
-                                mma_ts(tmem + 2 * PT + i * D, tmem + i * PT + kk * 8, v + (kk * 16 * 128 >> 4), id_o, (j | kk) != 0);
-                        }
-                        if (!ok) continue;
-                        if (j + 1 == steps[i]) {
-                            commit_elected(&bars->o_full[i]);
-                        } else {
-                            if (!have_k) ok = have_k = landed(2 * j + 2);
-                            if (ok) scores(i, j + 1);
-                            if (ok && j + 2 == steps[i]) commit_elected(&bars->q_empty[i]);      // its last scores
-                        }
+                        for (int kk = half * PT / 32; kk < (half + 1) * PT / 32; ++kk)
+                            mma_ts(t_o, t_s + kk * 8, v + (kk * 16 * 128 >> 4), id_o, (j | kk) != 0);
                     }
                     if (!ok) break;
                     commit_elected(&bars->empty[(tile + 2 * j + 1) % STAGES]);
-                    if (j + 1 < all) commit_elected(&bars->empty[(tile + 2 * j + 2) % STAGES]);
+                    if (j + 1 == steps) {
+                        commit_elected(&bars->o_full[i]);
+                    } else {
+                        ok = landed(2 * j + 2);
+                        if (ok) scores(j + 1);
+                        if (ok && j + 2 == steps) commit_elected(&bars->q_empty[i]);      // its last scores
+                    }
                 }
                 tile += 2 * all;
-                done[0] += steps[0];
-                done[1] += steps[1];
+                done += steps;
             }
             volatile int never = 0;
-            commit_elected(&bars->drain);
-            if (lane == 0) mbar_wait(&bars->drain, 0, &never, 0);
+            commit_elected(&bars->drain[i]);
+            if (lane == 0) mbar_wait(&bars->drain[i], 0, &never, 0);
             __syncwarp();
         }
     } else {
@@ -485,11 +488,13 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
         const uint32_t t_s = tmem + lanes + i * PT, t_o = tmem + lanes + 2 * PT + i * D;
         const float sl2 = p.scale_log2, raise = RAISE / sl2;
         int tile = 0, done = 0;                                 // tiles of the ring, steps of this tile before this work
+        int turns = 0;                                          // steps of both tiles before this work
         bool ok = true;
         PromptWork w;
         for (int n = 0; ok && take(n, &w); ++n) {
             const int steps = w.steps[i], cut0 = first_cut(w.seen), cut = first_cut(w.seen + i * PT);
             const int lim = w.seen + i * PT + quad * 32 + lane; // the last key the row sees
+            const int both = min(w.steps[0], w.steps[1]);
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
                 ok = ready(&bars->s_full[i], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
@@ -506,9 +511,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < PT; ++e)
                         if (e > seen) r[e >> 5][e & 31] = 0xFF800000u;  // -infinity
-                    ok = ready(&bars->scan[n & 1][j - cut0], (n >> 1) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                    ok = ready(&bars->scan[n % kWorkSlots][j - cut0], (n / kWorkSlots) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                     if (!ok) break;
-                    dirty = *static_cast<volatile int *>(&bars->dirty[n & 1][j - cut0]) != 0;
+                    dirty = *static_cast<volatile int *>(&bars->dirty[n % kWorkSlots][j - cut0]) != 0;
                     if (dirty && lane == 0) *static_cast<volatile int *>(&bars->skip[i]) = done + j;
                 }
                 auto x = [&](int e) { return __uint_as_float(r[e >> 5][e & 31]); };
@@ -535,6 +540,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         }
                     }
                 }
+                // The two tiles take turns at the exponentials (their warps share the special
+                // function units, and would fall in step: both at the exponentials, then both
+                // waiting for the tensor cores).  Nothing depends on it but time.
+                if (i == 0 ? j > 0 && j <= both : j < both)
+                    ok = ready(&bars->turn[1 - i][quad], (turns + j - (i == 0)) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                if (!ok) break;
                 // p = 2^(x * scale_log2 - m * scale_log2); a row that has seen nothing yet has all -inf
                 const float ref = m == -INFINITY ? 0.0f : -m * sl2;
                 const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(ref, ref);
@@ -558,6 +569,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
                     }
                 }
+                if (j < both && lane == 0) mbar_arrive(&bars->turn[i][quad]);
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
                 l += s2.x + s2.y;
                 tmem_wait_st();
@@ -617,6 +629,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             }
             tile += 2 * max(w.steps[0], w.steps[1]);
             done += steps;
+            turns += both;
             give_back(n);
         }
     }
