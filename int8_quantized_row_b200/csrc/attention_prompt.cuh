@@ -84,13 +84,14 @@ struct PromptWork {
 constexpr int kCuts = 3;
 __device__ __forceinline__ int first_cut(int seen) { return seen + 1 > 0 ? (seen + 1) / PT : 0; }
 
+constexpr int kEarly = 6;                      // of a step's eight MMAs over 16 keys of P, those that need not wait for the last
 constexpr int kWorkSlots = 4;                  // pieces of work known at a time
 // Barriers that complete once per piece of work have parity (work & 1); those of a
 // work slot (work / kWorkSlots) & 1.
 struct PromptBarriers {
     uint64_t full[10], empty[10];              // the K/V ring
     uint64_t q_full[2], q_empty[2];            // a tile's queries
-    uint64_t s_full[2], p_ready[2][2];         // scores; P: tile, half of the keys (once per step)
+    uint64_t s_full[2], p_ready[2][2];         // scores; P of the first kEarly * 16 keys, of the others (once per step)
     uint64_t o_full[2], o_empty[2];            // the sums
     uint64_t turn[2][4];                       // tile i's warp has done its exponentials: the other tile's may begin
     uint64_t asked[kWorkSlots][kCuts], scan[kWorkSlots][kCuts];      // V of a cut step: asked for, looked over
@@ -163,10 +164,14 @@ __device__ __forceinline__ void commit_elected(uint64_t *bar) {
         : "memory");
 }
 
-// A wait of a whole warp that is usually over already: all lanes look once (about 40
-// cycles; lane 0's look and its broadcast take 240), and only then lane 0 waits.
+// A wait of a whole warp.  All lanes look, about 40 cycles a look (a try_wait sleeps
+// until the barrier's phase ends or some time has passed); lane 0's look and its
+// broadcast, which the bounded wait is made of, take 240.
 __device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity, volatile int *abort, int code) {
-    return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || warp_wait(bar, parity, abort, code);
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return warp_wait(bar, parity, abort, code);
 }
 
 // P V of one step over the keys that each row sees, without the tensor cores: O (in
@@ -283,23 +288,46 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
         if (warp == 11) {
-            // -------------------------------------------------------- the work, this CTA's share of it:
-            // the longest tiles of a sequence first; neighbouring CTAs are the heads of one
-            // tile, which share keys and values
-            auto tiles = [&](int s) {
-                const int2 r = kv::row_range(p.cu_q, s, p.N);
-                return (r.y - r.x + PROMPT_ROWS - 1) / PROMPT_ROWS;
+            // -------------------------------------------------------- the work, this CTA's share of it.
+            // In order of their length (in 256 keys: the level), the longest pieces first, dealt to
+            // the CTAs there and back; neighbours are the heads of one tile, which share keys and
+            // values.  Sequence s has its tile t at level t + before(s), for each of its tiles.
+            auto span = [&](int s) {                         // its levels [x, y)
+                const int2 q = kv::row_range(p.cu_q, s, p.N), k = kv::row_range(p.cu_k, s, p.M);
+                const int nq = q.y - q.x, before = max(0, k.y - k.x - nq) / PROMPT_ROWS;
+                return make_int2(before, before + (nq + PROMPT_ROWS - 1) / PROMPT_ROWS);
             };
+            int level = 0;
+            long long base = 0, here = 0;                    // pieces (without heads) of the levels above, of this one
+            for (int s = lane; s < p.B; s += 32) {
+                const int2 v = span(s);
+                if (v.y > v.x) level = max(level, v.y);
+            }
+            level = static_cast<int>(kv::warp_max(level));   // one above the highest
             auto publish = [&](int n) {                      // false: there is no more, or the CTA gives up
-                const long long item = blockIdx.x + static_cast<long long>(n) * gridDim.x;
-                long long place = 0;
-                const int b = kv::find_item(item / p.Hq, p.B, &place, tiles);
+                const int turn = (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+                const long long item = turn + static_cast<long long>(n) * gridDim.x;
+                while (level >= 0 && item / p.Hq >= base + here) {
+                    base += here;
+                    --level;
+                    int count = 0;
+                    for (int s = lane; s < p.B; s += 32) {
+                        const int2 v = span(s);
+                        count += level >= v.x && level < v.y;
+                    }
+                    here = __reduce_add_sync(0xFFFFFFFFu, count);
+                }
                 PromptWork w{};
                 w.steps[0] = -1;
-                if (b >= 0) {
+                if (level >= 0) {
+                    long long place = 0;
+                    const int b = kv::find_item(item / p.Hq - base, p.B, &place, [&](int s) {
+                        const int2 v = span(s);
+                        return level >= v.x && level < v.y ? 1 : 0;
+                    });
                     const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
                     const int nq = qr.y - qr.x, off = kr.y - kr.x - nq;
-                    const int first = (tiles(b) - 1 - static_cast<int>(place)) * PROMPT_ROWS;
+                    const int first = (level - span(b).x) * PROMPT_ROWS;
                     w.row = qr.x + first;
                     w.rows = nq - first;
                     w.key = kr.x;
@@ -321,7 +349,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     mbar_arrive(&bars->work_full[slot]);
                 }
                 __syncwarp();
-                return b >= 0;
+                return level >= 0;
             };
             int tile = 0;                                    // tiles of the ring so far
             bool more = publish(0), ok = true;
@@ -450,27 +478,27 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         continue;
                     }
                     commit_elected(&bars->empty[(tile + 2 * j) % STAGES]);       // K_j: its scores are issued
+                    const bool more = j + 1 < steps;
                     const uint32_t v = desc_low(ring_base + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, Shape::CHUNK_BYTES);
-                    // the first 64 keys' P while the softmax warps are at the other 64
+                    // three quarters of P while the softmax warps are at the last one
+                    ok = landed(2 * j + 1) && (!more || landed(2 * j + 2));
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && ready(&bars->p_ready[i][half], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                        if (half == 0) ok = ok && landed(2 * j + 1);
+                    for (int part = 0; part < 2; ++part) {
+                        ok = ok && ready(&bars->p_ready[i][part], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                         if (!ok || (j >= cut && *static_cast<volatile int *>(&bars->skip[i]) == done + j)) continue;
                         tc_fence_after_sync();
 #pragma unroll
-                        for (int kk = half * PT / 32; kk < (half + 1) * PT / 32; ++kk)
+                        for (int kk = part ? kEarly : 0; kk < (part ? PT / 16 : kEarly); ++kk)
                             mma_ts(t_o, t_s + kk * 8, v + (kk * 16 * 128 >> 4), id_o, (j | kk) != 0);
                     }
                     if (!ok) break;
-                    commit_elected(&bars->empty[(tile + 2 * j + 1) % STAGES]);
-                    if (j + 1 == steps) {
-                        commit_elected(&bars->o_full[i]);
+                    if (more) {
+                        scores(j + 1);
+                        if (j + 2 == steps) commit_elected(&bars->q_empty[i]);   // its last scores
                     } else {
-                        ok = landed(2 * j + 2);
-                        if (ok) scores(j + 1);
-                        if (ok && j + 2 == steps) commit_elected(&bars->q_empty[i]);      // its last scores
+                        commit_elected(&bars->o_full[i]);
                     }
+                    commit_elected(&bars->empty[(tile + 2 * j + 1) % STAGES]);
                 }
                 tile += 2 * all;
                 done += steps;
@@ -555,6 +583,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     uint32_t out[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
+                        if (c == 3 && e == 6) {                 // by now the first three quarters are stored
+                            tmem_wait_st();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
+                        }
                         const float2 y = unpack2(fma2(pack2(x(32 * c + 2 * e), x(32 * c + 2 * e + 1)), sl22, ref2));
                         const float p0 = ex2(y.x), p1 = ex2(y.y);
                         sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
@@ -562,12 +596,6 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         out[e] = *reinterpret_cast<const uint32_t *>(&h2);
                     }
                     tmem_st16(t_s + 16 * c, out);
-                    if (c == 1) {
-                        tmem_wait_st();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
-                    }
                 }
                 if (j < both && lane == 0) mbar_arrive(&bars->turn[i][quad]);
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
