@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             auto publish = [&](int n) {                      // false: there is no more, or the CTA gives up
                 const int turn = (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
                 const long long item = turn + static_cast<long long>(n) * gridDim.x;
-                while (level >= 0 && item / p.Hq >= base + here) {
+                const long long piece = item >> 31 ? item / p.Hq : static_cast<uint32_t>(item) / static_cast<uint32_t>(p.Hq);
+                while (level >= 0 && piece >= base + here) {
                     base += here;
                     --level;
                     int count = 0;
@@ -321,17 +322,17 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 w.steps[0] = -1;
                 if (level >= 0) {
                     long long place = 0;
-                    const int b = kv::find_item(item / p.Hq - base, p.B, &place, [&](int s) {
+                    const int b = kv::find_item(piece - base, p.B, &place, [&](int s) {
                         const int2 v = span(s);
                         return level >= v.x && level < v.y ? 1 : 0;
                     });
                     const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
                     const int nq = qr.y - qr.x, off = kr.y - kr.x - nq;
-                    const int first = (level - span(b).x) * PROMPT_ROWS;
+                    const int first = (level - max(0, off) / PROMPT_ROWS) * PROMPT_ROWS;
                     w.row = qr.x + first;
                     w.rows = nq - first;
                     w.key = kr.x;
-                    w.head = static_cast<int>(item % p.Hq);
+                    w.head = static_cast<int>(item - piece * p.Hq);
                     w.seen = first + off;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -351,10 +352,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 __syncwarp();
                 return level >= 0;
             };
-            int tile = 0;                                    // tiles of the ring so far
-            bool more = publish(0), ok = true;
-            for (int n = 0; ok && more; ++n) {
-                more = publish(n + 1);
+            int tile = 0, given = 0;                         // tiles of the ring so far; pieces told
+            bool more = true, ok = true;
+            auto tell = [&] {
+                if (more && (more = publish(given))) ++given;
+            };
+            tell();
+            tell();                                          // a search hides behind the piece before it
+            for (int n = 0; ok && n < given; ++n) {
                 // infinities and NaN in V of the steps that a mask cuts
                 const int slot = n % kWorkSlots, parity = (n / kWorkSlots) & 1;
                 const PromptWork w = bars->work[slot];
@@ -382,6 +387,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     }
                 }
                 tile += 2 * all;
+                tell();
             }
         } else if (warp == 8) {
             // -------------------------------------------------------- producer
