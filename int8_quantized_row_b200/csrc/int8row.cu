@@ -1253,19 +1253,20 @@ i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long
     p.past = past;
     // n rows that start anywhere in a block touch at most (n + 126) / 64 blocks, and at most n
     const long long items = std::min<long long>(n_new, (n_new + 126ll * B) / kv::BLOCK);
-    const dim3 grid(static_cast<unsigned>(items), (2 * H + kv::WARPS - 1) / kv::WARPS);
+    const bool few = n_new <= 8ll * B;
+    const int jobs = few ? kv::WARPS : kv::WARPS / 4;           // per CTA
+    const dim3 grid(static_cast<unsigned>(items), (2 * H + jobs - 1) / jobs);
     const dim3 block(32 * kv::WARPS);
     // A warp that keeps a whole block in registers suits prompts (one read of
     // the rows); for a few rows per sequence the small form's occupancy does.
-    const bool few = n_new <= 8ll * B;
     if (D == 128 && few)
-        kv::kv_append_kernel<128, 2><<<grid, block, 0, stream>>>(p);
+        kv::kv_append_kernel<128, 2, 1><<<grid, block, 0, stream>>>(p);
     else if (D == 128)
-        kv::kv_append_kernel<128, 32><<<grid, block, 0, stream>>>(p);
+        kv::kv_append_kernel<128, 8, 4><<<grid, block, 0, stream>>>(p);
     else if (few)
-        kv::kv_append_kernel<64, 2><<<grid, block, 0, stream>>>(p);
+        kv::kv_append_kernel<64, 2, 1><<<grid, block, 0, stream>>>(p);
     else
-        kv::kv_append_kernel<64, 16><<<grid, block, 0, stream>>>(p);
+        kv::kv_append_kernel<64, 4, 4><<<grid, block, 0, stream>>>(p);
     I8R_LAUNCHED();
     return I8R_OK;
 }

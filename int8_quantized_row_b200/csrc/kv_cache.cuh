@@ -101,17 +101,29 @@ __device__ __forceinline__ uint32_t max_bits(const uint4 &v, uint32_t m) {
     return __vmaxu2(m, v.w & 0x7FFF7FFFu);
 }
 
+// |code| of one value, in bits 8..15 of the result: |x * inv| clamped to 127, plus
+// a half, cut to a whole number.  The sum with 2^15 is cut to a multiple of 2^-8,
+// towards zero, which never reaches the next whole number; so this is
+// round-half-away, without the conversions that run at an eighth of the rate.
+__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
+    return __float_as_uint(__fadd_rz(fminf(fabsf(__fmul_rn(x, inv)), 127.0f), 32768.5f));
+}
+
+// The codes of four values (two words of fp16 pairs), with the values' signs.
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) {
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&w0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&w1));
+    const uint32_t lo = __byte_perm(code_bits(f0.x, inv), code_bits(f0.y, inv), 0x0051);
+    const uint32_t hi = __byte_perm(code_bits(f1.x, inv), code_bits(f1.y, inv), 0x0051);
+    uint32_t sign;                                 // 0xFF where the value is negative
+    asm("prmt.b32 %0, %1, %2, 0xFDB9;" : "=r"(sign) : "r"(w0), "r"(w1));
+    // a byte's two's complement: inverted, plus one; no carry leaves its byte
+    const uint32_t a = __byte_perm(lo, hi, 0x5410) ^ sign;
+    return ((a & 0x7F7F7F7Fu) + (sign & 0x01010101u)) ^ (a & 0x80808080u);
+}
+
 __device__ __forceinline__ uint2 codes8(const uint4 &v, float inv) {
-    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-        const uint32_t a = static_cast<uint32_t>(quant_code(f.x, inv)) & 0xFFu;
-        const uint32_t b = static_cast<uint32_t>(quant_code(f.y, inv)) & 0xFFu;
-        out[e >> 1] |= (a | (b << 8)) << (16 * (e & 1));
-    }
-    return make_uint2(out[0], out[1]);
+    return make_uint2(codes4(v.x, v.y, inv), codes4(v.z, v.w, inv));
 }
 
 struct AppendParams {
@@ -135,18 +147,21 @@ __device__ __forceinline__ int touched_blocks(const AppendParams &p, int b) {
     return (past % BLOCK + (r.y - r.x) + BLOCK - 1) / BLOCK;
 }
 
-// One warp per (touched block, head, K or V).  kHold warp-wide loads (a load
-// covers 256/D rows) stay in registers between the absmax and the codes; rows
-// past them are read a second time.  kHold = 64*D/256 holds a whole block (128
-// registers at D = 128) for prompts; single tokens take a small one, so that
-// more warps fit an SM.
-template <int D, int kHold>
+// kTeam warps per (touched block, head, K or V), each with every kTeam-th
+// warp-wide load (256/D rows).  kHold loads a warp stay in registers between the
+// absmax and the codes; rows past them are read a second time.  Prompts take
+// teams of four that hold a block among them; single tokens one warp that holds
+// little, so that more jobs fit an SM.
+template <int D, int kHold, int kTeam>
 __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int LANES = D / 8;                   // lanes per row (16 bytes each)
     constexpr int RPL = 32 / LANES;                // rows per warp-wide load
     const int lane = threadIdx.x & 31;
     const int sub = lane / LANES, col = (lane % LANES) * 8;
-    const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
+    const int team = (threadIdx.x >> 5) / kTeam, part = (threadIdx.x >> 5) % kTeam;
+    const int job = blockIdx.y * (WARPS / kTeam) + team;
+    const int first = part * RPL + sub;            // the lane's first row; then every STEP rows
+    constexpr int STEP = kTeam * RPL;
     if (job >= 2 * p.c.H) return;
     const int kv = job & 1, head = job >> 1;
     long long place = 0;
@@ -169,24 +184,31 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const __grid_cons
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        const int r = k * RPL + sub;
+        const int r = k * STEP + first;
         v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (r < n) v[k] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv]));
     }
 #pragma unroll
     for (int k = 0; k < kHold; ++k) m = max_bits(v[k], m);
-    for (int r = kHold * RPL + sub; r < n; r += RPL)
+    for (int r = kHold * STEP + first; r < n; r += STEP)
         m = max_bits(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), m);
     m = warp_max(max(m & 0xFFFFu, m >> 16));
+    if constexpr (kTeam > 1) {
+        __shared__ uint32_t tops[WARPS];
+        if (lane == 0) tops[team * kTeam + part] = m;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kTeam) : "memory");     // (and all have read old)
+#pragma unroll
+        for (int k = 0; k < kTeam; ++k) m = max(m, tops[team * kTeam + k]);
+    }
     // non-negative floats order like their bits, and a NaN stays on top
     const uint32_t top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
     const bool grown = top > __float_as_uint(old);
     const float scale = grown ? __uint_as_float(top) : old;
-    if (lane == 0) p.c.scale[kv][at] = scale;
+    if (part == 0 && lane == 0) p.c.scale[kv][at] = scale;
     if (grown && old > 0.0f) {
         // the codes already there, four rows of D = 128 (eight of 64) a load
         const float ratio = __fdiv_rn(old, scale);
-        for (int e = lane * 16; e < o0 * D; e += 512) {
+        for (int e = (part * 32 + lane) * 16; e < o0 * D; e += 512 * kTeam) {
             uint4 q = *reinterpret_cast<const uint4 *>(dst + e);
             uint32_t *w = reinterpret_cast<uint32_t *>(&q);
 #pragma unroll
@@ -206,10 +228,10 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const __grid_cons
     dst += static_cast<size_t>(o0) * D + col;
 #pragma unroll
     for (int k = 0; k < kHold; ++k) {
-        const int r = k * RPL + sub;
+        const int r = k * STEP + first;
         if (r < n) *reinterpret_cast<uint2 *>(dst + r * D) = codes8(v[k], inv);
     }
-    for (int r = kHold * RPL + sub; r < n; r += RPL)
+    for (int r = kHold * STEP + first; r < n; r += STEP)
         *reinterpret_cast<uint2 *>(dst + r * D) =
             codes8(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), inv);
 }
