@@ -79,6 +79,12 @@ def parse(argv=None):
                          "int8_mixed_linear_chain call replayed from a CUDA graph (one JSON line; "
                          "not the one-line contract run)")
     ap.add_argument("--chain-t", type=int, default=16, help="tokens per projection for --chain")
+    ap.add_argument("--layer", action="store_true",
+                    help="time a whole 175B-shaped decoder layer (projections with bias, activation and residual, "
+                         "8-bit key/value cache, attention) instead of one linear; prints one JSON line")
+    ap.add_argument("--layer-batch", type=int, default=16, help="sequences for --layer")
+    ap.add_argument("--layer-new", type=int, default=1, help="new tokens per sequence for --layer (1: decode)")
+    ap.add_argument("--layer-past", type=int, default=2047, help="tokens per sequence already cached, for --layer")
     ap.add_argument("--parallel", default="replica", choices=["replica", "column"],
                     help="N>1 ranks: replica = an independent batch per GPU (weak scaling, the default); "
                          "column = one layer split by weight columns over the GPUs, Y all-gathered over NCCL "
@@ -872,8 +878,121 @@ def run_chain(args):
     print(json.dumps(line), flush=True)
 
 
+def run_layer(args):
+    """One decoder layer of the 175B shape (hidden 12288, 96 heads of 128): layer norm, qkv with
+    bias, append to the 8-bit cache, attention, output projection with bias and residual, layer
+    norm, fc1 with bias and relu, fc2 with bias and residual.  With one new token per sequence the
+    attention reads the cache (int8_attention_decode); with more it is int8_attention_prompt, over
+    keys and values read back from the cache when there are earlier tokens.  The layer is captured
+    once into a CUDA graph and replayed; each operator is also timed alone, from a graph of its own.
+    The two layer norms are torch's.  Weights and cache exceed L2."""
+    import torch
+    import int8_quantized_row_b200 as i8
+    dev = torch.device("cuda", 0)
+    pk = peaks()
+    B, new, past, alpha, H, D = args.layer_batch, args.layer_new, args.layer_past, 6.0, 96, 128
+    T, d, total = B * new, H * D, past + new
+    W = {}
+    for name, (K, N) in wl.SWEEP_LAYERS.items():
+        w16 = torch.from_numpy(wl.make_w(K, N, 0.01)).to(dev)
+        Wq, sW = i8.int8_quantize_weight_colwise(w16)
+        W[name] = (Wq, sW, None if args.variant == "wq" else w16, torch.zeros(N, dtype=torch.float16, device=dev))
+        del w16
+    g = torch.Generator(device=dev).manual_seed(0)
+    x = torch.randn(T, d, generator=g, device=dev).half()
+    # a layer norm's gain makes the outlier columns (0.1 %)
+    gain = torch.ones(d, dtype=torch.float16, device=dev)
+    gain[torch.from_numpy(wl.planted_columns(d, round(0.001 * d), 1)).to(dev)] = 20.0
+    pages = -(-total // i8.KV_BLOCK)
+    table = torch.randperm(B * pages, generator=g, device=dev).int().view(B, pages)
+    codes = [torch.randint(-127, 128, (B * pages, H, i8.KV_BLOCK, D), generator=g, device=dev, dtype=torch.int8)
+             for _ in range(2)]
+    scale = [torch.full((B * pages, H), 4.0, device=dev) for _ in range(2)]
+    count = lambda n: torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev)
+    cu, cu_all = count(new), count(total)
+    before = torch.full((B,), past, dtype=torch.int32, device=dev)
+    after = before + new
+    ws = torch.empty(max(i8.workspace(T, K, N, dev).numel() for K, N in wl.SWEEP_LAYERS.values()), dtype=torch.uint8,
+                     device=dev)
+    out = {n: torch.empty(T, N, dtype=torch.float16, device=dev) for n, (_, N) in wl.SWEEP_LAYERS.items()}
+    o = torch.empty(T, H, D, dtype=torch.float16, device=dev)
+    kv = [torch.empty(B * total, H, D, dtype=torch.float16, device=dev) for _ in range(2)] if new > 1 and past else None
+    q, k, v = out["qkv"].view(T, 3, H, D).unbind(1)
+    n1, n2 = torch.empty_like(x), torch.empty_like(x)
+
+    def linear(name, a, act="none", residual=None):
+        Wq, sW, w16, b = W[name]
+        i8.int8_mixed_linear_fused(a, Wq, sW, w16, alpha, bias=b, act=act, residual=residual, Y=out[name], workspace_buf=ws)
+
+    def norm(a, y):
+        y.copy_(torch.nn.functional.layer_norm(a, (d,), gain))
+
+    def attend():
+        if new == 1:
+            i8.int8_attention_decode(q, *codes, *scale, table, after, O=o)
+        else:
+            i8.int8_attention_prompt(q, *(kv or (k, v)), cu, cu_all, O=o)
+    stages = [("norm", lambda: norm(x, n1)),
+              ("qkv", lambda: linear("qkv", n1)),
+              ("kv_append", lambda: i8.int8_kv_append(k, v, cu, before, table, *codes, *scale))]
+    if kv:
+        stages.append(("kv_gather", lambda: i8.int8_kv_gather(*codes, *scale, cu_all, table, B * total, K=kv[0], V=kv[1])))
+    stages += [("attention", attend),
+               ("out", lambda: linear("out", o.view(T, d), residual=x)),
+               ("norm2", lambda: norm(out["out"], n2)),
+               ("fc1", lambda: linear("fc1", n2, act="relu")),
+               ("fc2", lambda: linear("fc2", out["fc1"], residual=out["out"]))]
+
+    def layer():
+        for _, f in stages:
+            f()
+    steps = min(args.steps, 200)
+    side = torch.cuda.Stream()
+
+    def replayed_ms(f):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                f()
+            side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            f()
+        for _ in range(max(3, args.warmup)):
+            graph.replay()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(steps):
+            graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        del graph
+        return a.elapsed_time(b) / steps
+    ms = replayed_ms(layer)
+    n0 = i8.int8_kernel_launch_count()
+    layer()
+    launches = i8.int8_kernel_launch_count() - n0
+    torch.cuda.synchronize()
+    alone = {name: replayed_ms(f) for name, f in stages}
+    weights = sum(K * N for K, N in wl.SWEEP_LAYERS.values())
+    cached = 2 * B * total * H * D                             # codes of the tokens' keys and values
+    line = {"metric": "175B decoder layer with an 8-bit key/value cache, CUDA-graph replay", "value": T / (ms * 1e-3),
+            "unit": "tokens/s through the layer", "ms_per_layer": ms, "steps": steps, "sequences": B, "new_tokens": new,
+            "past_tokens": past, "alpha": alpha, "variant": args.variant, "launches_per_layer": launches,
+            "weight_bytes": weights, "cache_bytes": cached,
+            "frac_hbm": (weights + cached) / (ms * 1e-3) / 1e9 / pk["hbm_gbs"] if new == 1 else None,
+            "linear_tops": 2.0 * T * weights / (ms * 1e-3) / 1e12,
+            "operator_ms": alone, "peak_hbm_gbs": pk["hbm_gbs"], "peak_src": pk["src"], "data": "synthetic, seeded",
+            "status": i8.int8_read_and_clear_device_status()}
+    print(json.dumps(line), flush=True)
+
+
 def main():
     args = parse()
+    if args.layer:
+        run_layer(args)
+        return
     if args.sweep:
         run_sweep_int4(args) if args.codec == "int4" else run_sweep(args)
         return
