@@ -411,8 +411,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     }
                     __syncwarp();
                 };
+                // K_0, Q, V_0: what the first scores need is free before V_0's place is
                 int k = 0;
-                for (; ok && k < 2 && k < 2 * all; ++k) load_kv(k);
+                for (; ok && k < 1 && k < 2 * all; ++k) load_kv(k);
                 for (int i = 0; ok && i < 2; ++i) {
                     ok = n == 0 || ready(&bars->q_empty[i], (n - 1) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
                     if (!ok) break;
