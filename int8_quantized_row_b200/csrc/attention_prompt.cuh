@@ -596,6 +596,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
                         }
+                        // the other tile's turn: told ahead of the end, for the time that the telling takes
+                        if (c == 3 && e == 6 && j < both && lane == 0) mbar_arrive(&bars->turn[i][quad]);
                         const float2 y = unpack2(fma2(pack2(x(32 * c + 2 * e), x(32 * c + 2 * e + 1)), sl22, ref2));
                         const float p0 = ex2(y.x), p1 = ex2(y.y);
                         sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
@@ -604,7 +606,6 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     }
                     tmem_st16(t_s + 16 * c, out);
                 }
-                if (j < both && lane == 0) mbar_arrive(&bars->turn[i][quad]);
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
                 l += s2.x + s2.y;
                 tmem_wait_st();
