@@ -45,9 +45,9 @@ namespace attn {
 constexpr int PT = 128;                        // query rows per tile, keys per step
 constexpr int PROMPT_ROWS = 2 * PT;            // query rows per CTA
 constexpr int PROMPT_THREADS = 384;            // 8 softmax warps and four others
-// Registers: 384 threads are launched with 168 each; the softmax warps take 224
-// (a row's 128 scores stay in them) and the other four 56.
-constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 224, OTHER_REGS = 56;
+// Registers: 384 threads are launched with 168 each; the softmax warps take 216
+// (a row's 128 scores stay in them) and the other four 72.
+constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * 128 <= PROMPT_LAUNCH_REGS * PROMPT_THREADS, "more registers than launched with");
 constexpr uint32_t PROMPT_TMEM = 512;
 constexpr float RAISE = 8.0f;                  // log2 of how far a row may exceed its reference
@@ -173,6 +173,12 @@ __device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity, volatile i
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     return warp_wait(bar, parity, abort, code);
 }
+
+// First row, within work n, of tile i's 128: the tiles change places from one piece of work
+// to the next.  The second 128 rows see one step more than the first, and a short piece has
+// no second 128: so the tile that had less of a piece has more of the next, and is already
+// at it while the other one finishes.
+__device__ __forceinline__ int place_of(int i, int n) { return (i ^ (n & 1)) * PT; }
 
 // P V of one step over the keys that each row sees, without the tensor cores: O (in
 // tensor memory at t_o; zeros before the first step) += sum over keys 0 .. seen of
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         // what the tile's last row sees
-                        const int keys = i * PT < w.rows ? min((i + 1) * PT, w.rows) + w.seen : 0;
+                        const int at = place_of(i, n), keys = at < w.rows ? min(at + PT, w.rows) + w.seen : 0;
                         w.steps[i] = keys > 0 ? (keys + PT - 1) / PT : 0;
                     }
                 }
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         mbar_arrive_expect_tx(&bars->q_full[i], w.steps[i] > 0 ? Shape::TILE_BYTES : 0);
                         for (int c = 0; w.steps[i] > 0 && c < Shape::CHUNKS; ++c)
                             tma_load_2d(smem + i * Shape::TILE_BYTES + c * Shape::CHUNK_BYTES, &map_q, &bars->q_full[i],
-                                        w.head * D + 64 * c, w.row + i * PT);
+                                        w.head * D + 64 * c, w.row + place_of(i, n));
                     }
                     q_loaded[i] = n;
                     __syncwarp();
@@ -527,8 +533,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
         bool ok = true;
         PromptWork w;
         for (int n = 0; ok && take(n, &w); ++n) {
-            const int steps = w.steps[i], cut0 = first_cut(w.seen), cut = first_cut(w.seen + i * PT);
-            const int lim = w.seen + i * PT + quad * 32 + lane; // the last key the row sees
+            const int steps = w.steps[i], cut0 = first_cut(w.seen), cut = first_cut(w.seen + place_of(i, n));
+            const int lim = w.seen + place_of(i, n) + quad * 32 + lane;     // the last key the row sees
             const int both = min(w.steps[0], w.steps[1]);
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
@@ -540,16 +546,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r[c]);
                 tmem_wait_ld();
                 // a step that every row of the tile sees whole needs no mask
-                bool dirty = false;
                 if (j >= cut) {
                     const int seen = lim - j * PT;              // columns 0 .. seen stay
 #pragma unroll
                     for (int e = 0; e < PT; ++e)
                         if (e > seen) r[e >> 5][e & 31] = 0xFF800000u;  // -infinity
-                    ok = ready(&bars->scan[n % kWorkSlots][j - cut0], (n / kWorkSlots) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
-                    if (!ok) break;
-                    dirty = *static_cast<volatile int *>(&bars->dirty[n % kWorkSlots][j - cut0]) != 0;
-                    if (dirty && lane == 0) *static_cast<volatile int *>(&bars->skip[i]) = done + j;
                 }
                 auto x = [&](int e) { return __uint_as_float(r[e >> 5][e & 31]); };
                 float top[4] = {x(0), x(1), x(2), x(3)};
@@ -577,9 +578,11 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 }
                 // The two tiles take turns at the exponentials (their warps share the special
                 // function units, and would fall in step: both at the exponentials, then both
-                // waiting for the tensor cores).  Nothing depends on it but time.
-                if (i == 0 ? j > 0 && j <= both : j < both)
-                    ok = ready(&bars->turn[1 - i][quad], (turns + j - (i == 0)) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                // waiting for the tensor cores); the one with the second 128 rows, which was done
+                // first with the work before, leads.  Nothing depends on it but time.
+                const int before = j - ((i ^ n) & 1);
+                if (before >= 0 && before < both)
+                    ok = ready(&bars->turn[1 - i][quad], (turns + before) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                 if (!ok) break;
                 // p = 2^(x * scale_log2 - m * scale_log2); a row that has seen nothing yet has all -inf
                 const float ref = m == -INFINITY ? 0.0f : -m * sl2;
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                             tmem_wait_st();
                             tc_fence_before_sync();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars->p_ready[i][0]);
+                            if (j < cut && lane == 0) mbar_arrive(&bars->p_ready[i][0]);
                         }
                         // the other tile's turn: told ahead of the end, for the time that the telling takes
                         if (c == 3 && e == 6 && j < both && lane == 0) mbar_arrive(&bars->turn[i][quad]);
@@ -609,11 +612,21 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 const float2 s2 = unpack2(add2(sum[0], sum[1]));
                 l += s2.x + s2.y;
                 tmem_wait_st();
+                bool dirty = false;
+                if (j >= cut) {                                 // what V holds is known by now, or soon
+                    ok = ready(&bars->scan[n % kWorkSlots][j - cut0], (n / kWorkSlots) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
+                    if (!ok) break;
+                    dirty = *static_cast<volatile int *>(&bars->dirty[n % kWorkSlots][j - cut0]) != 0;
+                    if (dirty && lane == 0) *static_cast<volatile int *>(&bars->skip[i]) = done + j;
+                }
                 if (dirty)
                     values_seen<D>(t_s, t_o, ring + (tile + 2 * j + 1) % STAGES * Shape::TILE_BYTES, j > 0, lim - j * PT);
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_ready[i][1]);
+                if (lane == 0) {
+                    if (j >= cut) mbar_arrive(&bars->p_ready[i][0]);
+                    mbar_arrive(&bars->p_ready[i][1]);
+                }
             }
             ok = ok && ready(&bars->o_full[i], n & 1, abort, I8R_DEV_TMEM_TIMEOUT);
             if (!ok) break;
@@ -624,8 +637,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             const bool none = steps == 0 || lim < 0;            // (then what tensor memory holds is not looked at)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             uint8_t *mine = out + warp * OUT_BYTES;
-            const int first = i * PT + quad * 32;
-            __half *dst = p.O + static_cast<size_t>(w.row + first + (lane >> 3)) * p.ldo + static_cast<size_t>(w.head) * D +
+            // (read again: the loop above has no register to spare)
+            const volatile PromptWork *again = &bars->work[n % kWorkSlots];
+            const int rows = again->rows, row0 = place_of(i, n) + quad * 32;
+            __half *dst = p.O + static_cast<size_t>(again->row + row0 + (lane >> 3)) * p.ldo + static_cast<size_t>(again->head) * D +
                           8 * (lane & 7);
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
@@ -658,14 +673,14 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 for (int k = 0; k < 8; ++k) {
                     const int row = 4 * k + (lane >> 3);
                     const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-                    if (first + row < w.rows)
+                    if (row0 + row < rows)
                         *reinterpret_cast<uint4 *>(dst + static_cast<size_t>(4 * k) * p.ldo + 64 * h) = v;
                 }
                 __syncwarp();
             }
-            tile += 2 * max(w.steps[0], w.steps[1]);
+            tile += 2 * max(again->steps[0], again->steps[1]);
+            turns += min(again->steps[0], again->steps[1]);
             done += steps;
-            turns += both;
             give_back(n);
         }
     }
