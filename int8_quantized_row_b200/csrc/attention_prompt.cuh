@@ -180,6 +180,10 @@ __device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity, volatile i
 // at it while the other one finishes.
 __device__ __forceinline__ int place_of(int i, int n) { return (i ^ (n & 1)) * PT; }
 
+__device__ __forceinline__ __half2 largest(__half2 m, uint32_t x) {
+    return __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2 *>(&x)));
+}
+
 // P V of one step over the keys that each row sees, without the tensor cores: O (in
 // tensor memory at t_o; zeros before the first step) += sum over keys 0 .. seen of
 // this lane's P (at t_s) and V's rows (128-byte-swizzled 64-column chunks).  For the
@@ -305,10 +309,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             };
             int level = 0;
             long long base = 0, here = 0;                    // pieces (without heads) of the levels above, of this one
+            int2 mine = make_int2(0, 0);                     // this lane's sequence, when a warp holds them all
             for (int s = lane; s < p.B; s += 32) {
-                const int2 v = span(s);
-                if (v.y > v.x) level = max(level, v.y);
+                mine = span(s);
+                if (mine.y > mine.x) level = max(level, mine.y);
             }
+            const bool few = p.B <= 32;
             level = static_cast<int>(kv::warp_max(level));   // one above the highest
             auto publish = [&](int n) {                      // false: there is no more, or the CTA gives up
                 const int turn = (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
@@ -317,8 +323,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 while (level >= 0 && piece >= base + here) {
                     base += here;
                     --level;
-                    int count = 0;
-                    for (int s = lane; s < p.B; s += 32) {
+                    int count = few && level >= mine.x && level < mine.y;
+                    for (int s = lane; s < p.B && !few; s += 32) {
                         const int2 v = span(s);
                         count += level >= v.x && level < v.y;
                     }
@@ -327,11 +333,19 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 PromptWork w{};
                 w.steps[0] = -1;
                 if (level >= 0) {
-                    long long place = 0;
-                    const int b = kv::find_item(piece - base, p.B, &place, [&](int s) {
-                        const int2 v = span(s);
-                        return level >= v.x && level < v.y ? 1 : 0;
-                    });
+                    int b;
+                    if (few) {                               // the (piece - base)-th sequence that has a tile here
+                        const bool here_too = level >= mine.x && level < mine.y;
+                        const unsigned set = __ballot_sync(0xFFFFFFFFu, here_too);
+                        const int rank = __popc(set & ((1u << lane) - 1u));
+                        b = __ffs(__ballot_sync(0xFFFFFFFFu, here_too && rank == static_cast<int>(piece - base))) - 1;
+                    } else {
+                        long long place = 0;
+                        b = kv::find_item(piece - base, p.B, &place, [&](int s) {
+                            const int2 v = span(s);
+                            return level >= v.x && level < v.y ? 1 : 0;
+                        });
+                    }
                     const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
                     const int nq = qr.y - qr.x, off = kr.y - kr.x - nq;
                     const int first = (level - max(0, off) / PROMPT_ROWS) * PROMPT_ROWS;
@@ -375,7 +389,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                     // turn from the one two before: once the producer has asked for this one,
                     // it is the one that full[] completes next.
                     ok = ready(&bars->asked[slot][c], parity, abort, I8R_DEV_PIPELINE_TIMEOUT);
-                    uint32_t top[4] = {0u, 0u, 0u, 0u};      // largest magnitudes, as bits
+                    // largest magnitudes; a NaN stays
+                    __half2 top[4] = {};
                     if (ok && cut + c < all) {
                         const int k = tile + 2 * (cut + c) + 1;
                         ok = ready(&bars->full[k % STAGES], (k / STAGES) & 1, abort, I8R_DEV_PIPELINE_TIMEOUT);
@@ -383,10 +398,17 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 #pragma unroll 4
                         for (int e = 0; e < Shape::TILE_BYTES / 512; e += 4)
 #pragma unroll
-                            for (int z = 0; z < 4; ++z) top[z] = kv::max_bits(v[(e + z) * 32], top[z]);
+                            for (int z = 0; z < 4; ++z) {
+                                const uint4 x = v[(e + z) * 32];
+                                top[0] = largest(top[0], x.x);
+                                top[1] = largest(top[1], x.y);
+                                top[2] = largest(top[2], x.z);
+                                top[3] = largest(top[3], x.w);
+                            }
                     }
-                    const uint32_t m = __vmaxu2(__vmaxu2(top[0], top[1]), __vmaxu2(top[2], top[3]));
-                    const bool bad = __any_sync(0xFFFFFFFFu, (m >> 16) >= 0x7C00u || (m & 0xFFFFu) >= 0x7C00u);
+                    const __half2 all4 = __hmax2_nan(__hmax2_nan(top[0], top[1]), __hmax2_nan(top[2], top[3]));
+                    const uint32_t m = *reinterpret_cast<const uint32_t *>(&all4);
+                    const bool bad = __any_sync(0xFFFFFFFFu, (m >> 16 & 0x7FFFu) >= 0x7C00u || (m & 0x7FFFu) >= 0x7C00u);
                     if (lane == 0) {
                         bars->dirty[slot][c] = bad;
                         mbar_arrive(&bars->scan[slot][c]);
@@ -634,6 +656,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             // O / l in fp16, 64 columns at a time through shared memory (piece e, 16 bytes, of
             // row r in place e ^ (r % 8)), so that whole lines are written.  A row that sees no
             // key is zeros, whatever its tile's steps left.
+            // A warp that has no row of the sequence only says that it has looked.
             const bool none = steps == 0 || lim < 0;            // (then what tensor memory holds is not looked at)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             uint8_t *mine = out + warp * OUT_BYTES;
@@ -642,8 +665,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             const int rows = again->rows, row0 = place_of(i, n) + quad * 32;
             __half *dst = p.O + static_cast<size_t>(again->row + row0 + (lane >> 3)) * p.ldo + static_cast<size_t>(again->head) * D +
                           8 * (lane & 7);
+            if (row0 >= rows) {
+                tc_fence_before_sync();
+                if (lane == 0) mbar_arrive(&bars->o_empty[i]);
+            }
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
+            for (int h = 0; h < D / 64 && row0 < rows; ++h) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     uint32_t o[32];
