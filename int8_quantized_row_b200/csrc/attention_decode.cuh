@@ -15,10 +15,16 @@
 //
 // The codes travel by cp.async into the warp's own slots, four sub-tiles of 16
 // tokens: as K's are read, V's are asked for, and as V's are read, the next
-// block's K.  With 12 warps that is 48 to 96 KB on the way to every SM.  A lane's bytes are its own mma.sync
-// fragments: m16n8k16 with tokens (then V's columns) as the 16 rows and queries as
-// the 8 columns, which suits one to eight queries per head; at one MMA in ten
-// cycles the legacy tensor path is nowhere near a limit.
+// block's K.  With 12 warps that is 48 to 96 KB on the way to every SM.  A lane's
+// bytes are its own mma.sync fragments: m16n8k16 with tokens (then V's columns) as
+// the 16 rows and queries as the 8 columns, which suits one to eight queries per
+// head; at one MMA in ten cycles the legacy tensor path is nowhere near a limit
+// (128 rows of a tcgen05 product would be mostly empty).
+//
+// Measured: 16 sequences of 2048 tokens, 96 heads of 128: 145 us (805 MB, 5.5 TB/s,
+// 85 % of a copy's rate); 16 of 0 to 2048, 15000 tokens in all: 78 us (4.7 TB/s: about
+// ten of them are the start, the joins and the uneven end); 64 long ones, 12 queries a
+// head: 262 us (4.4 TB/s, bound by instructions); one of 1000 tokens, 40 heads: 12 us.
 //
 // What counts besides bytes is instructions, most of them to turn codes into fp16:
 // xor 0x80 and a byte permute against 0x64 make 1024 + (code + 128), exactly.  For V
@@ -78,7 +84,6 @@ __host__ __device__ constexpr size_t decode_smem(int tile, int D, int warps) {
 // queries 8 of 255 (12, with the queries' fragments read from shared memory for
 // every 32 tokens, were slower: 289 us for 269 on 64 long sequences of 12 queries a head).
 __host__ __device__ constexpr int dec_warps(int nt) { return nt == 1 ? 12 : 8; }
-constexpr int DEC_MAX_WARPS = dec_warps(1);
 constexpr size_t DEC_SMEM = 226 * 1024;
 static_assert(decode_smem(8, 128, dec_warps(1)) <= DEC_SMEM && decode_smem(16, 128, dec_warps(2)) <= DEC_SMEM, "the widest tiles fit");
 static_assert(piece_floats(8, 64) * 4 <= ring_bytes(8, 64) && piece_floats(16, 64) * 4 <= ring_bytes(16, 64) &&
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
     __syncthreads();
 
     // Merge this CTA's pieces, item by item in order; an item that begins or ends
-    // in another CTA leaves one piece for combine_kernel, in slot 0 if it begins
+    // in another CTA leaves one piece for attention_combine_kernel, in slot 0 if it begins
     // where the CTA's range does, else in slot 1.
     auto piece_of = [&](int k) {
         return (k & 1) ? reinterpret_cast<float *>(smem + (k >> 1) * warp_ring)

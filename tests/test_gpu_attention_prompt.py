@@ -77,6 +77,18 @@ def test_packed_prompts(Hq, H, D):
     assert device_status_clean()
 
 
+@pytest.mark.parametrize("B,Hq,D", [(32, 5, 64), (33, 7, 128), (150, 3, 64), (300, 2, 128)])
+def test_many_prompts(B, Hq, D):
+    """More sequences than a warp has lanes, and than four each; several pieces of work for every CTA."""
+    n = [(37 * b) % 190 for b in range(B)]
+    n[B // 2] = 600
+    nk = [a + (b % 3) * 50 for b, a in enumerate(n)]
+    Q, K, V = inputs(B, n, nk, Hq, 1, D)
+    O = i8.int8_attention_prompt(Q, K, V, cum(n), cum(nk))
+    check(O, Q, K, V, n, nk, D ** -0.5)
+    assert device_status_clean()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_keys_from_before_the_queries_and_rows_that_see_none(D):
     nq = [1, 10, 200, 300, 7, 400, 129, 64, 0]
