@@ -1255,12 +1255,13 @@ i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long
     // n rows that start anywhere in a block touch at most (n + 126) / 64 blocks, and at most n
     const long long items = std::min<long long>(n_new, (n_new + 126ll * B) / kv::BLOCK);
     const bool few = n_new <= 8ll * B;
-    const int jobs = few ? kv::WARPS : kv::WARPS / 4;           // per CTA
+    const int jobs = few ? kv::WARPS : 2 * (kv::WARPS / 4);      // per CTA
     const dim3 grid(static_cast<unsigned>(items), (2 * H + jobs - 1) / jobs);
     const dim3 block(32 * kv::WARPS);
     // Four warps that keep a whole block in registers among them suit prompts (one
-    // read of the rows: 65 us for 4096 tokens of 96 heads); for up to eight rows a
-    // sequence a warp a block does (16 tokens: 8 us).
+    // read of the rows: 59 us for 4096 tokens of 96 heads), with two jobs each for one
+    // search (one: 65 us, four: 61, eight: 70); for up to eight rows a sequence a warp
+    // a block does (16 tokens: 8 to 10 us).
     if (D == 128 && few)
         kv::kv_append_kernel<128, 2, 1><<<grid, block, 0, stream>>>(p);
     else if (D == 128)

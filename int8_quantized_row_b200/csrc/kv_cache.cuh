@@ -9,10 +9,10 @@
 //
 // Both kernels are bound by HBM for prompts: append reads 2 bytes and writes 1
 // per value, read-back reads 1 and writes 2.  4096 tokens of 96 heads of 128:
-// append 65 us (4.6 TB/s; one warp a block and the division-like conversions of
-// the general code took 123), read-back 59 us (5.1 TB/s).  Single tokens are
-// bound by latency: 8 us for 16 sequences, the chain of finding the block, its
-// scale and its rows.
+// append 59 us (5.1 TB/s; one warp a block, and the rounding with conversions that
+// run at an eighth of the rate, took 123), read-back 59 us (5.1 TB/s).  Single
+// tokens are bound by latency: 8 to 10 us for 16 sequences, the chain of finding
+// the block, its scale and its rows.
 #pragma once
 
 #include "device_common.cuh"
@@ -162,11 +162,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4) kv_append_kernel(const __grid_c
     const int lane = threadIdx.x & 31;
     const int sub = lane / LANES, col = (lane % LANES) * 8;
     const int team = (threadIdx.x >> 5) / kTeam, part = (threadIdx.x >> 5) % kTeam;
-    const int job = blockIdx.y * (WARPS / kTeam) + team;
     const int first = part * RPL + sub;            // the lane's first row; then every STEP rows
     constexpr int STEP = kTeam * RPL;
-    if (job >= 2 * p.c.H) return;
-    const int kv = job >= p.c.H, head = job - kv * p.c.H;        // neighbours share lines of their rows
     long long place = 0;
     const int b = find_item(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
     if (b < 0) return;
@@ -178,69 +175,75 @@ __global__ void __launch_bounds__(32 * WARPS, 4) kv_append_kernel(const __grid_c
     // tokens [t0, t1) of the sequence are new and in this block
     const int t0 = max(past, i * BLOCK), t1 = min(past + (range.y - range.x), (i + 1) * BLOCK);
     const int o0 = t0 - i * BLOCK, n = t1 - t0;                 // offset of the first new row; rows
-    const __half *src = p.x[kv] + static_cast<size_t>(range.x + (t0 - past)) * p.ld[kv] + head * D + col;
-    const size_t at = static_cast<size_t>(page) * p.c.H + head;
-    int8_t *dst = p.c.codes[kv] + at * BLOCK * D;
-    const float old = o0 > 0 ? p.c.scale[kv][at] : 0.0f;
+    // the block's heads, K's and then V's: neighbours, whose rows share lines, side by side
+    [[maybe_unused]] int turn = 0;
+    for (int job = blockIdx.y * (WARPS / kTeam) + team; job < 2 * p.c.H; job += gridDim.y * (WARPS / kTeam)) {
+        const int kv = job >= p.c.H, head = job - kv * p.c.H;
+        const __half *src = p.x[kv] + static_cast<size_t>(range.x + (t0 - past)) * p.ld[kv] + head * D + col;
+        const size_t at = static_cast<size_t>(page) * p.c.H + head;
+        int8_t *dst = p.c.codes[kv] + at * BLOCK * D;
+        const float old = o0 > 0 ? p.c.scale[kv][at] : 0.0f;
 
-    uint4 v[kHold];
-    uint32_t m = 0;
+        uint4 v[kHold];
+        uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-        const int r = k * STEP + first;
-        v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n) v[k] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv]));
-    }
-#pragma unroll
-    for (int k = 0; k < kHold; ++k) m = max_bits(v[k], m);
-    for (int r = kHold * STEP + first; r < n; r += STEP)
-        m = max_bits(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), m);
-    m = warp_max(max(m & 0xFFFFu, m >> 16));
-    if constexpr (kTeam > 1) {
-        __shared__ uint32_t tops[WARPS];
-        if (lane == 0) tops[team * kTeam + part] = m;
-        static_assert(WARPS == 2 * kTeam, "two teams");
-        if (team == 0)                             // (and all have read old)
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * kTeam) : "memory");
-        else
-            asm volatile("bar.sync 2, %0;" ::"n"(32 * kTeam) : "memory");
-#pragma unroll
-        for (int k = 0; k < kTeam; ++k) m = max(m, tops[team * kTeam + k]);
-    }
-    // non-negative floats order like their bits, and a NaN stays on top
-    const uint32_t top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
-    const bool grown = top > __float_as_uint(old);
-    const float scale = grown ? __uint_as_float(top) : old;
-    if (part == 0 && lane == 0) p.c.scale[kv][at] = scale;
-    if (grown && old > 0.0f) {
-        // the codes already there, four rows of D = 128 (eight of 64) a load
-        const float ratio = __fdiv_rn(old, scale);
-        for (int e = (part * 32 + lane) * 16; e < o0 * D; e += 512 * kTeam) {
-            uint4 q = *reinterpret_cast<const uint4 *>(dst + e);
-            uint32_t *w = reinterpret_cast<uint32_t *>(&q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t out = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float c = static_cast<float>(static_cast<int8_t>((w[j] >> (8 * k)) & 0xFFu));
-                    out |= (static_cast<uint32_t>(quant_code(c, ratio)) & 0xFFu) << (8 * k);
-                }
-                w[j] = out;
-            }
-            *reinterpret_cast<uint4 *>(dst + e) = q;
+        for (int k = 0; k < kHold; ++k) {
+            const int r = k * STEP + first;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < n) v[k] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv]));
         }
-    }
-    const float inv = recip127(scale);
-    dst += static_cast<size_t>(o0) * D + col;
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-        const int r = k * STEP + first;
-        if (r < n) *reinterpret_cast<uint2 *>(dst + r * D) = codes8(v[k], inv);
+        for (int k = 0; k < kHold; ++k) m = max_bits(v[k], m);
+        for (int r = kHold * STEP + first; kHold * STEP < BLOCK && r < n; r += STEP)
+            m = max_bits(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), m);
+        m = warp_max(max(m & 0xFFFFu, m >> 16));
+        if constexpr (kTeam > 1) {
+            __shared__ uint32_t tops[2][WARPS];      // in turn: a warp may be a job ahead
+            if (lane == 0) tops[turn][team * kTeam + part] = m;
+            static_assert(WARPS == 2 * kTeam, "two teams");
+            if (team == 0)                             // (and all have read old)
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kTeam) : "memory");
+            else
+                asm volatile("bar.sync 2, %0;" ::"n"(32 * kTeam) : "memory");
+#pragma unroll
+            for (int k = 0; k < kTeam; ++k) m = max(m, tops[turn][team * kTeam + k]);
+            turn ^= 1;
+        }
+        // non-negative floats order like their bits, and a NaN stays on top
+        const uint32_t top = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+        const bool grown = top > __float_as_uint(old);
+        const float scale = grown ? __uint_as_float(top) : old;
+        if (part == 0 && lane == 0) p.c.scale[kv][at] = scale;
+        if (grown && old > 0.0f) {
+            // the codes already there, four rows of D = 128 (eight of 64) a load
+            const float ratio = __fdiv_rn(old, scale);
+            for (int e = (part * 32 + lane) * 16; e < o0 * D; e += 512 * kTeam) {
+                uint4 q = *reinterpret_cast<const uint4 *>(dst + e);
+                uint32_t *w = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t out = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float c = static_cast<float>(static_cast<int8_t>((w[j] >> (8 * k)) & 0xFFu));
+                        out |= (static_cast<uint32_t>(quant_code(c, ratio)) & 0xFFu) << (8 * k);
+                    }
+                    w[j] = out;
+                }
+                *reinterpret_cast<uint4 *>(dst + e) = q;
+            }
+        }
+        const float inv = recip127(scale);
+        dst += static_cast<size_t>(o0) * D + col;
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) {
+            const int r = k * STEP + first;
+            if (r < n) *reinterpret_cast<uint2 *>(dst + r * D) = codes8(v[k], inv);
+        }
+        for (int r = kHold * STEP + first; kHold * STEP < BLOCK && r < n; r += STEP)
+            *reinterpret_cast<uint2 *>(dst + r * D) =
+                codes8(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), inv);
     }
-    for (int r = kHold * STEP + first; r < n; r += STEP)
-        *reinterpret_cast<uint2 *>(dst + r * D) =
-            codes8(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * p.ld[kv])), inv);
 }
 
 struct GatherParams {
