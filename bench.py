@@ -912,8 +912,8 @@ def run_layer(args):
     cu, cu_all = count(new), count(total)
     before = torch.full((B,), past, dtype=torch.int32, device=dev)
     after = before + new
-    ws = torch.empty(max(i8.workspace(T, K, N, dev).numel() for K, N in wl.SWEEP_LAYERS.values()), dtype=torch.uint8,
-                     device=dev)
+    size = i8.int8_mixed_linear_wq_workspace_size if args.variant == "wq" else i8.int8_mixed_linear_workspace_size
+    ws = torch.empty(max(size(T, K, N) for K, N in wl.SWEEP_LAYERS.values()), dtype=torch.uint8, device=dev)
     out = {n: torch.empty(T, N, dtype=torch.float16, device=dev) for n, (_, N) in wl.SWEEP_LAYERS.items()}
     o = torch.empty(T, H, D, dtype=torch.float16, device=dev)
     kv = [torch.empty(B * total, H, D, dtype=torch.float16, device=dev) for _ in range(2)] if new > 1 and past else None
