@@ -316,6 +316,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             int level = 0;
             long long base = 0, here = 0;                    // pieces (without heads) of the levels above, of this one
             int2 mine = make_int2(0, 0);                     // this lane's sequence, when a warp holds them all
+            int from = 0;                                    // else how far the search on this level has come
+            long long passed = 0;
             for (int s = lane; s < p.B; s += 32) {
                 mine = span(s);
                 if (mine.y > mine.x) level = max(level, mine.y);
@@ -335,6 +337,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         count += level >= v.x && level < v.y;
                     }
                     here = __reduce_add_sync(0xFFFFFFFFu, count);
+                    from = 0;
+                    passed = 0;
                 }
                 PromptWork w{};
                 w.steps[0] = -1;
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                         b = kv::find_item(piece - base, p.B, &place, [&](int s) {
                             const int2 v = span(s);
                             return level >= v.x && level < v.y ? 1 : 0;
-                        });
+                        }, &from, &passed);
                     }
                     const int2 qr = kv::row_range(p.cu_q, b, p.N), kr = kv::row_range(p.cu_k, b, p.M);
                     const int nq = qr.y - qr.x, off = kr.y - kr.x - nq;

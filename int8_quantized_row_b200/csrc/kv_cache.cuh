@@ -46,12 +46,14 @@ __device__ __forceinline__ int block_of(const int32_t *table, int max_blocks, in
 // Which sequence item `item` belongs to, and its place there, when sequence b
 // has count(b) items: a warp adds 128 sequences' counts at a time, four
 // consecutive ones a lane (their loads are in flight together).  Returns -1
-// past the last item.  All lanes get the same answer.
+// past the last item.  All lanes get the same answer.  The search begins at
+// sequence *from (a multiple of 128), which *before items precede, and leaves both
+// where it ended: a search for a later item may go on from there.
 template <typename Count>
-__device__ __forceinline__ int find_item(long long item, int B, long long *place, Count &&count) {
+__device__ __forceinline__ int find_item(long long item, int B, long long *place, Count &&count, int *from, long long *before) {
     const int lane = threadIdx.x & 31;
-    long long base = 0;
-    for (int b0 = 0; b0 < B; b0 += 128) {
+    long long base = *before;
+    for (int b0 = *from; b0 < B; b0 += 128) {
         int n[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) n[j] = b0 + 4 * lane + j < B ? count(b0 + 4 * lane + j) : 0;
@@ -70,10 +72,63 @@ __device__ __forceinline__ int find_item(long long item, int B, long long *place
             for (int k = 0; k < 3; ++k)
                 if (j == k && left >= n[k]) left -= n[k], j = k + 1;
             const int at = __ffs(past) - 1;
+            *from = b0;
+            *before = base;
             *place = __shfl_sync(0xFFFFFFFFu, left, at);
             return __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + j, at);
         }
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    return -1;
+}
+
+template <typename Count>
+__device__ __forceinline__ int find_item(long long item, int B, long long *place, Count &&count) {
+    int from = 0;
+    long long before = 0;
+    return find_item(item, B, place, count, &from, &before);
+}
+
+// The same by a whole CTA of WARPS warps, 128 sequences a warp at a time; every
+// thread of the CTA calls it.
+template <typename Count>
+__device__ __forceinline__ int find_item_cta(long long item, int B, long long *place, Count &&count) {
+    if (B <= 128) return find_item(item, B, place, count);      // one look: each warp for itself
+    __shared__ long long sums[2][WARPS], found_place;
+    __shared__ int found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    long long base = 0;
+    for (int b0 = 0, turn = 0; b0 < B; b0 += 128 * WARPS, turn ^= 1) {
+        const int mine = b0 + 128 * warp + 4 * lane;
+        int n[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = mine + j < B ? count(mine + j) : 0;
+        long long sum = static_cast<long long>(n[0]) + n[1] + n[2] + n[3];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (lane == 0) sums[turn][warp] = sum;
+        __syncthreads();
+        long long before = base;
+        int hit = -1;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (hit < 0 && item < base + sums[turn][w]) hit = w, before = base;
+            base += sums[turn][w];
+        }
+        if (hit >= 0) {
+            if (warp == hit) {                                   // this warp's 128 again, to the sequence
+                int from = b0 + 128 * warp;
+                long long at = 0;
+                const int b = find_item(item, B, &at, count, &from, &before);
+                if (lane == 0) {
+                    found = b;
+                    found_place = at;
+                }
+            }
+            __syncthreads();
+            *place = found_place;
+            return found;
+        }
     }
     return -1;
 }
@@ -165,7 +220,7 @@ __global__ void __launch_bounds__(32 * WARPS, 4) kv_append_kernel(const __grid_c
     const int first = part * RPL + sub;            // the lane's first row; then every STEP rows
     constexpr int STEP = kTeam * RPL;
     long long place = 0;
-    const int b = find_item(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
+    const int b = find_item_cta(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
     if (b < 0) return;
     const int2 range = row_range(p.cu_new, b, p.n_new);
     const int past = p.past[b];
@@ -262,14 +317,13 @@ __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const __grid_cons
     const int lane = threadIdx.x & 31;
     const int sub = lane / LANES, col = (lane % LANES) * 8;
     const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
-    if (job >= 2 * p.c.H) return;
-    const int kv = job >= p.c.H, head = job - kv * p.c.H;        // neighbours share lines of their rows
     long long place = 0;
-    const int b = find_item(blockIdx.x, p.B, &place, [&](int s) {
+    const int b = find_item_cta(blockIdx.x, p.B, &place, [&](int s) {
         const int2 r = row_range(p.cu, s, p.rows);
         return (r.y - r.x + BLOCK - 1) / BLOCK;
     });
-    if (b < 0) return;
+    if (b < 0 || job >= 2 * p.c.H) return;
+    const int kv = job >= p.c.H, head = job - kv * p.c.H;        // neighbours share lines of their rows
     const int2 range = row_range(p.cu, b, p.rows);
     const int i = static_cast<int>(place);
     const int page = block_of(p.c.table, p.c.max_blocks, p.c.num_blocks, b, i);

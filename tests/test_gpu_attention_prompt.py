@@ -77,7 +77,7 @@ def test_packed_prompts(Hq, H, D):
     assert device_status_clean()
 
 
-@pytest.mark.parametrize("B,Hq,D", [(32, 5, 64), (33, 7, 128), (150, 3, 64), (300, 2, 128)])
+@pytest.mark.parametrize("B,Hq,D", [(32, 5, 64), (33, 7, 128), (150, 3, 64), (300, 2, 128), (900, 1, 64)])
 def test_many_prompts(B, Hq, D):
     """More sequences than a warp has lanes, and than four each; several pieces of work for every CTA."""
     n = [(37 * b) % 190 for b in range(B)]

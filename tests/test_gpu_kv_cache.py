@@ -227,6 +227,28 @@ def test_many_sequences():
         assert np.array_equal(c.cpu().numpy().astype(np.float64), w.codes)
 
 
+@pytest.mark.parametrize("B,longest", [(128, 3), (129, 3), (1024, 3), (1025, 3), (2500, 3), (1300, 40)])
+def test_more_sequences_than_a_search_sees_at_once(B, longest):
+    rng = np.random.default_rng(B)
+    past = [int(v) for v in rng.integers(0, 70, B)]
+    new = [int(v) for v in rng.integers(0, longest, B)]
+    new[-1] = 1                                            # the last one of all has its row
+    s = Setup(B, past, new, 3, 64)
+    codes, scale = s.device()
+    s.append(codes, scale)
+    want = s.want()
+    rows = int(s.all[-1])
+    K, V = i8.int8_kv_gather(*codes, *scale, dev(s.all), dev(s.table), rows)
+    for c, sc, o, w in zip(codes, scale, (K, V), want):
+        assert np.array_equal(sc.cpu().numpy().astype(np.float64), w.scale)
+        assert np.array_equal(c.cpu().numpy().astype(np.float64), w.codes)
+        o = o.cpu().numpy()
+        for b in range(0, B, 7):
+            assert np.array_equal(o[s.all[b]:s.all[b + 1]], w.gather(s.table[b], past[b] + new[b]))
+        assert np.array_equal(o[s.all[B - 1]:], w.gather(s.table[B - 1], past[B - 1] + new[B - 1]))
+    assert device_status_clean()
+
+
 @pytest.mark.parametrize("what", ["block", "negative block", "past", "past beyond the table", "rows", "order"])
 def test_bad_indexes_are_reported_and_skipped(what):
     s = Setup(10, [5, 70], [40, 30], 2, 64)
