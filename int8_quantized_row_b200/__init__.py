@@ -210,9 +210,9 @@ class _on:
             self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
             self._handle = stream.cuda_stream
         else:
-            if torch.cuda.current_device() != device:
+            if torch._C._cuda_getDevice() != device:
                 self._contexts = (torch.cuda.device(device),)
-            # current_stream(device).cuda_stream, without the 2 us of making a Stream
+            # current_device(), and current_stream(device).cuda_stream without the 2 us of making a Stream
             self._handle = torch._C._cuda_getCurrentRawStream(device)
 
     def __enter__(self):
@@ -225,13 +225,13 @@ class _on:
             c.__exit__(*exc)
 
 
-def _workspace(workspace_buf, size, device):
-    """A buffer of `size` bytes, and its address and bytes; or the caller's."""
+def _workspace(workspace_buf, size, device, like):
+    """A buffer of `size` bytes where `like` is, and its address and bytes; or the caller's."""
     import torch
     if workspace_buf is None:
-        workspace_buf = torch.empty(max(1, size), dtype=torch.uint8, device=device)
-    elif workspace_buf.get_device() != device.index:
-        _wrong(workspace_buf, "workspace_buf", device.index, workspace_buf.dtype)
+        workspace_buf = like.new_empty(max(1, size), dtype=torch.uint8)
+    elif workspace_buf.get_device() != device:
+        _wrong(workspace_buf, "workspace_buf", device, workspace_buf.dtype)
     return workspace_buf, workspace_buf.data_ptr(), workspace_buf.numel() * workspace_buf.element_size()
 
 
@@ -315,9 +315,9 @@ def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none
     r = None if residual is None else _at(residual, "residual", d, f16, (T, N))
     so = lib()
     with _on(d, stream) as handle:
-        Y = torch.empty((T, N), dtype=f16, device=X.device) if Y is None else Y
+        Y = X.new_empty((T, N)) if Y is None else Y
         size = so.int8_mixed_linear_wq_workspace_size if W16 is None else so.int8_mixed_linear_workspace_size
-        ws, at, nbytes = _workspace(workspace_buf, 0 if workspace_buf is not None else size(T, K, N), X.device)
+        ws, at, nbytes = _workspace(workspace_buf, 0 if workspace_buf is not None else size(T, K, N), d, X)
         _check("int8_mixed_linear_fused", so.int8_mixed_linear_fused(
             x, T, K, wq, sw, w16, N, alpha, b, ACTIVATIONS[act], r, _at(Y, "Y", d, f16, (T, N)), at, nbytes, handle))
     return Y
@@ -557,8 +557,8 @@ def int8_kv_gather(Kc, Vc, sK, sV, cu, block_table, rows, K=None, V=None, stream
     c = _at(cu, "cu", d, torch.int32, (B + 1,))
     shape = (int(rows), H, D)
     with _on(d, stream) as handle:
-        K = torch.empty(shape, dtype=torch.float16, device=Kc.device) if K is None else K
-        V = torch.empty(shape, dtype=torch.float16, device=Kc.device) if V is None else V
+        K = Kc.new_empty(shape, dtype=torch.float16) if K is None else K
+        V = Kc.new_empty(shape, dtype=torch.float16) if V is None else V
         _check("int8_kv_gather", lib().int8_kv_gather(
             *cache, H, D, *table, c, B, shape[0], _at(K, "K", d, torch.float16, shape),
             _at(V, "V", d, torch.float16, shape), handle))
@@ -584,9 +584,9 @@ def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O
     n = _at(lengths, "lengths", d, torch.int32, (B,))
     so = lib()
     with _on(d, stream) as handle:
-        O = torch.empty(shape, dtype=torch.float16, device=Q.device) if O is None else O
+        O = Q.new_empty(shape) if O is None else O
         size = 0 if workspace_buf is not None else so.int8_attention_decode_workspace_size(Hq, H, D)
-        ws, at, nbytes = _workspace(workspace_buf, size, Q.device)
+        ws, at, nbytes = _workspace(workspace_buf, size, d, Q)
         o, ldo = _rows(O, "O", d, torch.float16, shape)
         _check("int8_attention_decode", so.int8_attention_decode(
             q, ldq, B, Hq, H, D, *cache, *table, n, D ** -0.5 if scale is None else scale, o, ldo, at, nbytes, handle))
@@ -611,7 +611,7 @@ def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=N
     cq = _at(cu_q, "cu_q", d, torch.int32, (max(B, 0) + 1,))
     ck = cq if cu_k is None else _at(cu_k, "cu_k", d, torch.int32, (B + 1,))
     with _on(d, stream) as handle:
-        O = torch.empty((N, Hq, D), dtype=f16, device=Q.device) if O is None else O
+        O = Q.new_empty((N, Hq, D)) if O is None else O
         o, ldo = _rows(O, "O", d, f16, (N, Hq, D))
         _check("int8_attention_prompt", lib().int8_attention_prompt(
             q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, D ** -0.5 if scale is None else scale, o, ldo, handle))
