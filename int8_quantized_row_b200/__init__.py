@@ -37,6 +37,7 @@ _L = ctypes.c_longlong
 _Z = ctypes.c_size_t
 
 _lib = None
+torch = None        # bound by lib(): importing this module, as a build does, does not load it
 
 
 class I8RError(RuntimeError):
@@ -51,7 +52,7 @@ class I8RError(RuntimeError):
 
 def lib():
     """The loaded C library (ctypes.CDLL) with argument types declared."""
-    global _lib
+    global _lib, torch
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -112,6 +113,8 @@ def lib():
                  "int4_quantize_weight_groupwise", "int4_dequantize_weight", "int4_linear", "int8_kv_append",
                  "int8_kv_gather", "int8_attention_decode", "int8_attention_prompt"):
         getattr(so, name).restype = _I
+    import torch as module
+    torch = module
     _lib = so
     return so
 
@@ -145,7 +148,6 @@ def _dev(t, dtype, name, ndim=None):
 # and hand plain integers to ctypes.
 
 def _wrong(t, name, device, dtype):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -188,46 +190,45 @@ def _rows(t, name, device, dtype, shape):
 
 def _device_of(t, name, ndim):
     """Index of the CUDA device of a tensor of `ndim` dimensions."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    try:
+        device = t.get_device()
+    except AttributeError:
+        device = -1
+    if device < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    return t.get_device()
+    return device
 
 
-class _on:
-    """With this device current and, where the call names a stream, allocations made on that
-    stream: a buffer that the call frees at its end is not handed out again before its
-    kernels ran.  Gives the stream's handle."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._contexts = ()
-        if stream is not None:
-            if stream.device_index != device:
-                raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
-            self._contexts = (torch.cuda.device(device), torch.cuda.stream(stream))
-            self._handle = stream.cuda_stream
-        else:
-            if torch._C._cuda_getDevice() != device:
-                self._contexts = (torch.cuda.device(device),)
-            # current_device(), and current_stream(device).cuda_stream without the 2 us of making a Stream
-            self._handle = torch._C._cuda_getCurrentRawStream(device)
+class _Here:
+    """The context of a call on the current device and stream: nothing to do."""
 
     def __enter__(self):
-        for c in self._contexts:
-            c.__enter__()
-        return self._handle
+        pass
 
     def __exit__(self, *exc):
-        for c in reversed(self._contexts):
-            c.__exit__(*exc)
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(device, stream):
+    """A stream's handle, and the context to make the call in: this device current and, where
+    the call names a stream, allocations made on that stream (a buffer that the call frees at
+    its end is not handed out again before its kernels ran)."""
+    if stream is None:
+        # current_device(), and current_stream(device).cuda_stream without the 2 us of making a Stream
+        here = torch._C._cuda_getDevice() == device
+        return torch._C._cuda_getCurrentRawStream(device), _HERE if here else torch.cuda.device(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)          # (which makes its device current too)
 
 
 def _workspace(workspace_buf, size, device, like):
     """A buffer of `size` bytes where `like` is, and its address and bytes; or the caller's."""
-    import torch
     if workspace_buf is None:
         workspace_buf = like.new_empty(max(1, size), dtype=torch.uint8)
     elif workspace_buf.get_device() != device:
@@ -301,7 +302,7 @@ def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none
     """Y fp16 [T,N] = act(XW + bias) + residual, XW the LLM.int8() linear of X fp16 [T,K]
     (W16 None: the Wq-only variant).  bias fp16 [N], residual fp16 [T,N] (may be Y itself),
     act one of "none", "relu", "gelu"."""
-    import torch
+    so = lib()
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
     f16 = torch.float16
@@ -313,8 +314,8 @@ def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none
     w16 = None if W16 is None else _at(W16, "W16", d, f16, (K, N))
     b = None if bias is None else _at(bias, "bias", d, f16, (N,))
     r = None if residual is None else _at(residual, "residual", d, f16, (T, N))
-    so = lib()
-    with _on(d, stream) as handle:
+    handle, there = _on(d, stream)
+    with there:
         Y = X.new_empty((T, N)) if Y is None else Y
         size = so.int8_mixed_linear_wq_workspace_size if W16 is None else so.int8_mixed_linear_workspace_size
         ws, at, nbytes = _workspace(workspace_buf, 0 if workspace_buf is not None else size(T, K, N), d, X)
@@ -521,7 +522,6 @@ def int4_linear(X, W4, S4, N, Y=None, workspace_buf=None, stream=None):
 def _cache_args(d, Kc, Vc, sK, sV, block_table):
     """The C arguments of a cache on device d, checked: (Kc, Vc, sK, sV, num_blocks), (H, D),
     (table, max_blocks), B."""
-    import torch
     blocks, H, _, D = Kc.shape
     codes, scales = (blocks, H, KV_BLOCK, D), (blocks, H)
     if block_table.dim() != 2:
@@ -536,7 +536,7 @@ def int8_kv_append(K, V, cu_new, past, block_table, Kc, Vc, sK, sV, stream=None)
     """Add rows cu_new[b]..cu_new[b+1]-1 of K, V (fp16 [n,H,D], rows may be strided) to sequence b
     of the cache (Kc, Vc int8 [blocks,H,64,D], sK, sV fp32 [blocks,H]), which holds past[b]
     tokens.  cu_new int32 [B+1], past int32 [B], block_table int32 [B,max_blocks]."""
-    import torch
+    so = lib()
     d = _device_of(Kc, "Kc", 4)
     cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
     _device_of(K, "K", 3)
@@ -544,22 +544,24 @@ def int8_kv_append(K, V, cu_new, past, block_table, Kc, Vc, sK, sV, stream=None)
     k, ldk = _rows(K, "K", d, torch.float16, rows)
     v, ldv = _rows(V, "V", d, torch.float16, rows)
     cu, p = _at(cu_new, "cu_new", d, torch.int32, (B + 1,)), _at(past, "past", d, torch.int32, (B,))
-    with _on(d, stream) as handle:
-        _check("int8_kv_append", lib().int8_kv_append(k, ldk, v, ldv, rows[0], H, D, cu, p, B, *cache, *table, handle))
+    handle, there = _on(d, stream)
+    with there:
+        _check("int8_kv_append", so.int8_kv_append(k, ldk, v, ldv, rows[0], H, D, cu, p, B, *cache, *table, handle))
 
 
 def int8_kv_gather(Kc, Vc, sK, sV, cu, block_table, rows, K=None, V=None, stream=None):
     """-> (K, V) fp16 [rows,H,D]: tokens 0.. of sequence b of the cache in rows cu[b]..cu[b+1]-1
     (cu int32 [B+1]; rows behind cu[B] are not written)."""
-    import torch
+    so = lib()
     d = _device_of(Kc, "Kc", 4)
     cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
     c = _at(cu, "cu", d, torch.int32, (B + 1,))
     shape = (int(rows), H, D)
-    with _on(d, stream) as handle:
+    handle, there = _on(d, stream)
+    with there:
         K = Kc.new_empty(shape, dtype=torch.float16) if K is None else K
         V = Kc.new_empty(shape, dtype=torch.float16) if V is None else V
-        _check("int8_kv_gather", lib().int8_kv_gather(
+        _check("int8_kv_gather", so.int8_kv_gather(
             *cache, H, D, *table, c, B, shape[0], _at(K, "K", d, torch.float16, shape),
             _at(V, "V", d, torch.float16, shape), handle))
     return K, V
@@ -574,7 +576,7 @@ def int8_attention_decode_workspace_size(Hq, H, D):
 def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O=None, workspace_buf=None, stream=None):
     """O fp16 [B,Hq,D]: attention of one query token per sequence (Q fp16 [B,Hq,D], rows may be
     strided) over the first lengths[b] tokens of the 8-bit cache.  scale defaults to 1/sqrt(D)."""
-    import torch
+    so = lib()
     d = _device_of(Kc, "Kc", 4)
     cache, (H, D), table, B = _cache_args(d, Kc, Vc, sK, sV, block_table)
     _device_of(Q, "Q", 3)
@@ -582,8 +584,8 @@ def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O
     shape = (B, Hq, D)
     q, ldq = _rows(Q, "Q", d, torch.float16, shape)
     n = _at(lengths, "lengths", d, torch.int32, (B,))
-    so = lib()
-    with _on(d, stream) as handle:
+    handle, there = _on(d, stream)
+    with there:
         O = Q.new_empty(shape) if O is None else O
         size = 0 if workspace_buf is not None else so.int8_attention_decode_workspace_size(Hq, H, D)
         ws, at, nbytes = _workspace(workspace_buf, size, d, Q)
@@ -598,7 +600,7 @@ def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=N
     (rows may be strided); sequence b has query rows cu_q[b]..cu_q[b+1]-1 and key rows
     cu_k[b]..cu_k[b+1]-1 (cu_k defaults to cu_q), the last of each aligned.  scale defaults to
     1/sqrt(D).  Rows of O that belong to no sequence are not written."""
-    import torch
+    so = lib()
     d = _device_of(Q, "Q", 3)
     _device_of(K, "K", 3)
     _device_of(cu_q, "cu_q", 1)
@@ -610,9 +612,10 @@ def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=N
     B = cu_q.shape[0] - 1
     cq = _at(cu_q, "cu_q", d, torch.int32, (max(B, 0) + 1,))
     ck = cq if cu_k is None else _at(cu_k, "cu_k", d, torch.int32, (B + 1,))
-    with _on(d, stream) as handle:
+    handle, there = _on(d, stream)
+    with there:
         O = Q.new_empty((N, Hq, D)) if O is None else O
         o, ldo = _rows(O, "O", d, f16, (N, Hq, D))
-        _check("int8_attention_prompt", lib().int8_attention_prompt(
+        _check("int8_attention_prompt", so.int8_attention_prompt(
             q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, D ** -0.5 if scale is None else scale, o, ldo, handle))
     return O
