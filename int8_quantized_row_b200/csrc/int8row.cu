@@ -1262,14 +1262,16 @@ i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long
     // read of the rows: 59 us for 4096 tokens of 96 heads), with two jobs each for one
     // search (one: 65 us, four: 61, eight: 70); for up to eight rows a sequence a warp
     // a block does (16 tokens: 8 to 10 us).
+    auto launch = [&](auto kernel) { kernel<<<grid, block, 0, stream>>>(p); };
+    const bool many = B > 128;
     if (D == 128 && few)
-        kv::kv_append_kernel<128, 2, 1><<<grid, block, 0, stream>>>(p);
+        launch(many ? kv::kv_append_kernel<128, 2, 1, true> : kv::kv_append_kernel<128, 2, 1, false>);
     else if (D == 128)
-        kv::kv_append_kernel<128, 8, 4><<<grid, block, 0, stream>>>(p);
+        launch(many ? kv::kv_append_kernel<128, 8, 4, true> : kv::kv_append_kernel<128, 8, 4, false>);
     else if (few)
-        kv::kv_append_kernel<64, 2, 1><<<grid, block, 0, stream>>>(p);
+        launch(many ? kv::kv_append_kernel<64, 2, 1, true> : kv::kv_append_kernel<64, 2, 1, false>);
     else
-        kv::kv_append_kernel<64, 4, 4><<<grid, block, 0, stream>>>(p);
+        launch(many ? kv::kv_append_kernel<64, 4, 4, true> : kv::kv_append_kernel<64, 4, 4, false>);
     I8R_LAUNCHED();
     return I8R_OK;
 }
@@ -1295,10 +1297,11 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
     p.cu = cu;
     const long long items = std::min<long long>(rows, (rows + 63ll * B) / kv::BLOCK);
     const dim3 grid(static_cast<unsigned>(items), (2 * H + kv::WARPS - 1) / kv::WARPS);
+    auto launch = [&](auto kernel) { kernel<<<grid, 32 * kv::WARPS, 0, stream>>>(p); };
     if (D == 128)
-        kv::kv_gather_kernel<128><<<grid, 32 * kv::WARPS, 0, stream>>>(p);
+        launch(B > 128 ? kv::kv_gather_kernel<128, true> : kv::kv_gather_kernel<128, false>);
     else
-        kv::kv_gather_kernel<64><<<grid, 32 * kv::WARPS, 0, stream>>>(p);
+        launch(B > 128 ? kv::kv_gather_kernel<64, true> : kv::kv_gather_kernel<64, false>);
     I8R_LAUNCHED();
     return I8R_OK;
 }

@@ -90,10 +90,11 @@ __device__ __forceinline__ int find_item(long long item, int B, long long *place
 }
 
 // The same by a whole CTA of WARPS warps, 128 sequences a warp at a time; every
-// thread of the CTA calls it.
+// thread of the CTA calls it.  For more than 128 sequences (kMany: append for 4096 of
+// one token, 8 heads, 278 -> 94 us); up to there, where each warp has one look, the
+// kernels without it are 1 us faster.
 template <typename Count>
 __device__ __forceinline__ int find_item_cta(long long item, int B, long long *place, Count &&count) {
-    if (B <= 128) return find_item(item, B, place, count);      // one look: each warp for itself
     __shared__ long long sums[2][WARPS], found_place;
     __shared__ int found;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -210,7 +211,7 @@ __device__ __forceinline__ int touched_blocks(const AppendParams &p, int b) {
 // absmax and the codes; rows past them are read a second time.  Prompts take
 // teams of four that hold a block among them; single tokens one warp that holds
 // little, so that more jobs fit an SM.
-template <int D, int kHold, int kTeam>
+template <int D, int kHold, int kTeam, bool kMany>
 __global__ void __launch_bounds__(32 * WARPS, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int LANES = D / 8;                   // lanes per row (16 bytes each)
     constexpr int RPL = 32 / LANES;                // rows per warp-wide load
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(32 * WARPS, 4) kv_append_kernel(const __grid_c
     const int first = part * RPL + sub;            // the lane's first row; then every STEP rows
     constexpr int STEP = kTeam * RPL;
     long long place = 0;
-    const int b = find_item_cta(blockIdx.x, p.B, &place, [&](int s) { return touched_blocks(p, s); });
+    auto blocks = [&](int s) { return touched_blocks(p, s); };
+    const int b = kMany ? find_item_cta(blockIdx.x, p.B, &place, blocks) : find_item(blockIdx.x, p.B, &place, blocks);
     if (b < 0) return;
     const int2 range = row_range(p.cu_new, b, p.n_new);
     const int past = p.past[b];
@@ -309,7 +311,7 @@ struct GatherParams {
 };
 
 // One warp per (block, head, K or V): fp16_rn(code * fl32(scale/127)).
-template <int D>
+template <int D, bool kMany>
 __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const __grid_constant__ GatherParams p) {
     constexpr int LANES = D / 8;
     constexpr int RPL = 32 / LANES;
@@ -318,10 +320,11 @@ __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const __grid_cons
     const int sub = lane / LANES, col = (lane % LANES) * 8;
     const int job = blockIdx.y * WARPS + (threadIdx.x >> 5);
     long long place = 0;
-    const int b = find_item_cta(blockIdx.x, p.B, &place, [&](int s) {
+    auto blocks = [&](int s) {
         const int2 r = row_range(p.cu, s, p.rows);
         return (r.y - r.x + BLOCK - 1) / BLOCK;
-    });
+    };
+    const int b = kMany ? find_item_cta(blockIdx.x, p.B, &place, blocks) : find_item(blockIdx.x, p.B, &place, blocks);
     if (b < 0 || job >= 2 * p.c.H) return;
     const int kv = job >= p.c.H, head = job - kv * p.c.H;        // neighbours share lines of their rows
     const int2 range = row_range(p.cu, b, p.rows);
