@@ -335,10 +335,10 @@ void int4_debug_set_product_path(int mode);
  *   which holds past[b] tokens, for each of B sequences.  K and V are fp16
  *   [n_new, H, D]: head h of row r starts at element r*ld + h*D (ldk, ldv >=
  *   H*D, multiples of 8), so they may be slices of a projection's output.
- *   past and cu_new are not changed.  The blocks that one call writes must be
- *   different ones for different sequences (the call does not check this), and
- *   calls that write the same block must not overlap on the GPU.  n_new = 0 or
- *   B = 0 is a no-op.
+ *   past and cu_new are not changed.  The blocks that one call writes must all be
+ *   different, within a sequence and between sequences (the call does not check
+ *   this; a block named twice holds a mixture), and calls that write the same
+ *   block must not overlap on the GPU.  n_new = 0 or B = 0 is a no-op.
  * int8_kv_gather: K, V [rows, H, D] fp16 from the cache: tokens 0 .. len-1 of
  *   sequence b go to rows cu[b] .. cu[b+1]-1, with len = cu[b+1] - cu[b], each
  *   value fp16_rn(code * fl32(s / 127)).  Rows behind cu[B] are not touched.

@@ -216,3 +216,39 @@ def test_a_captured_layer_replays_token_after_token(Hq, H, D):
     for a, b in zip(graphed.codes + graphed.scale, eager.codes + eager.scale):
         assert torch.equal(a, b)
     assert device_status_clean()
+
+
+def test_two_streams_at_once():
+    """Prompts on one stream while tokens are made on another, each with its own cache: the same
+    bits as one after the other."""
+    layer = Layer(4, 2, 128, seed=8)
+    lens, B, rounds = [300, 17, 129], 6, 6
+    xs = [hidden(layer, sum(lens), 20 + r) for r in range(rounds)]
+    start = hidden(layer, B, 40)
+    ones = cum([1] * B)
+    first = Cache(layer, B, 300, seed=4)
+    prompt(layer, first, hidden(layer, 6 * 40, 41), [40] * 6)
+
+    def prompts(out):
+        for x in xs:
+            out.append(prompt(layer, Cache(layer, len(lens), 300, seed=5), x, lens))
+
+    def tokens(cache, out):
+        x = start
+        for _ in range(4 * rounds):
+            x = token(layer, cache, x, ones)[2]
+            out.append(x)
+    want = [[], []]
+    prompts(want[0])
+    tokens(first.clone(), want[1])
+    cache, got = first.clone(), [[], []]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        prompts(got[0])
+    with torch.cuda.stream(streams[1]):
+        tokens(cache, got[1])
+    torch.cuda.synchronize()
+    for a, b in zip(got[0] + got[1], want[0] + want[1]):
+        assert torch.equal(a, b)
+    assert device_status_clean()
