@@ -243,3 +243,16 @@ def test_binding_refusals():
     with pytest.raises(i8.I8RError):
         f(Q, K, V, cu, scale=float("nan"))
     assert f(Q[:0], K, V, cum([0])).shape == (0, 4, 64)
+
+
+def test_rows_far_apart():
+    """Rows 2^25 elements apart: offsets past 32 bits in every tensor."""
+    n, D = 130, 64
+    Q, K, V = inputs(3, [n], [n], 1, 1, D)
+    wide = torch.empty(n, 2 ** 25, dtype=torch.float16, device="cuda")          # 8.7 GB
+    far = [wide[:, at:at + D].view(n, 1, D) for at in (0, 2 ** 23, 2 ** 24, 3 * 2 ** 23)]
+    for t, x in zip(far, (Q, K, V)):
+        t.copy_(x)
+    i8.int8_attention_prompt(*far[:3], cum([n]), O=far[3])
+    assert torch.equal(far[3], i8.int8_attention_prompt(Q, K, V, cum([n])))
+    assert device_status_clean()

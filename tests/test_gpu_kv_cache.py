@@ -301,3 +301,25 @@ def test_binding_refusals():
         call(K=wide[:, :128].unflatten(1, (2, 64)))
     call(K=K[:0], V=V[:0])                                                             # nothing to add
     assert device_status_clean()
+
+
+def test_offsets_past_32_bits():
+    """Blocks past 2^32 codes, and rows 2^25 elements apart."""
+    H, D, rows = 1, 128, 130
+    blocks = 2 ** 32 // (H * BLOCK * D) + 4
+    s = Setup(21, [0], [rows], H, D, spare=0)
+    codes, scale = s.device()
+    s.append(codes, scale)
+    near = i8.int8_kv_gather(*codes, *scale, dev(s.all), dev(s.table), rows)
+    big = [torch.empty(blocks, H, BLOCK, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    big_scale = [torch.empty(blocks, H, device="cuda") for _ in range(2)]
+    table = dev(np.array([[blocks - 1, 5, blocks - 3]], np.int32))
+    wide = torch.empty(rows, 2 ** 25, dtype=torch.float16, device="cuda")       # 8.7 GB
+    K, V = (wide[:, at:at + D].view(rows, H, D) for at in (0, 2 ** 24))
+    K.copy_(dev(s.x[0]))
+    V.copy_(dev(s.x[1]))
+    i8.int8_kv_append(K, V, dev(s.cu), dev(np.array([0], np.int32)), table, *big, *big_scale)
+    far = i8.int8_kv_gather(*big, *big_scale, dev(s.all), table, rows)
+    for a, b in zip(near, far):
+        assert torch.equal(a, b)
+    assert device_status_clean()
