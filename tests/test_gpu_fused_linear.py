@@ -203,3 +203,28 @@ def test_binding_refusals():
         f(Xd, Wq, sW, Wd, float("nan"))
     with pytest.raises(i8.I8RError):
         f(Xd, Wq, sW, Wd, workspace_buf=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 128, 200])
+def test_a_residual_that_the_call_before_has_just_written(T):
+    X, W, bias, _ = inputs(T, 1024, 1024, seed=T)
+    x, w, b = (torch.from_numpy(a).cuda() for a in (X, W, bias))
+    Wq, sW = i8.int8_quantize_weight_colwise(w)
+    residual, Y = (torch.zeros(T, 1024, dtype=torch.float16, device="cuda") for _ in range(2))
+
+    def both(sync):
+        for k in range(20):
+            i8.int8_mixed_linear_fused(x, Wq, sW, w, 6.0, bias=b if k % 2 else None, act="relu", residual=Y, Y=residual)
+            if sync:
+                torch.cuda.synchronize()
+            i8.int8_mixed_linear_fused(x, Wq, sW, w, 6.0, residual=residual, act="gelu", Y=Y)
+            if sync:
+                torch.cuda.synchronize()
+            Y.mul_(0.25)
+        return Y.clone()
+    want = both(True)
+    for _ in range(5):
+        residual.zero_()
+        Y.zero_()
+        assert torch.equal(both(False), want)
+    assert bool(torch.isfinite(want).all()) and device_status_clean()
