@@ -27,12 +27,11 @@
 // head: 262 us (4.4 TB/s, bound by instructions); one of 1000 tokens, 40 heads: 12 us.
 //
 // What counts besides bytes is instructions, most of them to turn codes into fp16:
-// xor 0x80 and a byte permute against 0x64 make 1024 + (code + 128), exactly.  For V
-// a subtraction takes the 1152 off again.  For K they stay in the operand and the
-// scores start at -1152 sum(Q) instead, which costs fp32 sums of that size: an error
-// of about 1152 * 2^-24 = 0.00007 of a code per step, before the scale, where the
-// codec itself rounds to half a code (V's sums, which become the output, are kept
-// exact).  p = e^(x - max) <= 1 is rounded to fp16 (2^-11) for the second product,
+// xor 0x80 and a byte permute against 0x64 make 1024 + (code + 128), exactly, and a
+// subtraction takes the 1152 off again.  (Left in K's operand and taken off the sums
+// instead, it costs fp32 sums of the size of 1152 |sum(Q)|: scores that are 0.001 to
+// 0.003 off where the queries' mean is 3 to 8, and saves nothing: 264 us for 266 on 64
+// long sequences of 12 queries a head.)  p = e^(x - max) <= 1 is rounded to fp16 (2^-11) for the second product,
 // as the output will be, and the softmax's sum is that of the rounded p (one more
 // MMA, with ones for V).  The sums over V are kept in units of the current block's
 // scale, so the MMAs accumulate in place.
@@ -115,18 +114,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Two codes as fp16, 1152 too large: their bytes of x = codes ^ 0x80 are picked
-// into the low bytes of 0x6400, 1024 + byte.
-constexpr float kCodeBias = 1152.0f;
+// Two codes as fp16: their bytes of x = codes ^ 0x80 are picked into the low bytes
+// of 0x6400, 1024 + byte, which is 1152 more than the code.
 template <int kSel>
-__device__ __forceinline__ uint32_t biased_codes(uint32_t x) {
-    return __byte_perm(x, 0x64646464u, kSel);
-}
-// The same, exactly the codes.
-template <int kSel>
-__device__ __forceinline__ uint32_t exact_codes(uint32_t x) {
-    const uint32_t u = biased_codes<kSel>(x);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(kCodeBias));
+__device__ __forceinline__ uint32_t code_pair(uint32_t x) {
+    const uint32_t u = __byte_perm(x, 0x64646464u, kSel);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
@@ -356,7 +349,6 @@ struct State {
     float acc[D / 16][NT][4];            // in units of vs
     float m[NT][2], l[NT][2];            // of this lane's queries 2t, 2t + 1: the same in all its g
     float vs;                            // the scale acc is in (sV/127 of the last block with any)
-    float start[NT][2];                  // -1152 sum(Q): what a score starts at
     uint2 q[D / 16][NT];                 // the queries' fragments
 
     // a new item: nothing summed yet
@@ -377,25 +369,16 @@ struct State {
 
     // its queries, once they have come
     __device__ __forceinline__ void take_queries(const DecodeParams &p, const uint8_t *queries) {
-        const int lane = threadIdx.x & 31, t = lane & 3;
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float sum = 0.0f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint2 v = reinterpret_cast<const uint2 *>(queries + (k * NT + n) * 256)[lane];
                 v.x ^= p.negate;
                 v.y ^= p.negate;
                 q[k][n] = v;
-                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x));
-                const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-                sum += (a.x + a.y) + (b.x + b.y);
             }
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) start[n][e] = -kCodeBias * __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4 * e);
-        }
     }
 
     // Scores of sub-tiles j and j + 1: rows are tokens g and g+8, a lane's four
@@ -410,10 +393,7 @@ struct State {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[s][n][e] = start[n][e & 1];
-                    y[s][n][e] = 0.0f;
-                }
+                for (int e = 0; e < 4; ++e) x[s][n][e] = y[s][n][e] = 0.0f;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
             uint32_t a[2][4], b[2][4];
@@ -430,8 +410,8 @@ struct State {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const uint32_t u = a[s][k] ^ 0x80808080u, v = b[s][k] ^ 0x80808080u;
-                    const uint32_t a0 = biased_codes<0x4140>(u), a2 = biased_codes<0x4342>(u);
-                    const uint32_t a1 = biased_codes<0x4140>(v), a3 = biased_codes<0x4342>(v);
+                    const uint32_t a0 = code_pair<0x4140>(u), a2 = code_pair<0x4342>(u);
+                    const uint32_t a1 = code_pair<0x4140>(v), a3 = code_pair<0x4342>(v);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         mma16816(NT == 1 && (k & 1) ? y[s][n] : x[s][n], a0, a1, a2, a3, q[4 * c + k][n].x, q[4 * c + k][n].y);
@@ -533,8 +513,8 @@ struct State {
             for (int half = 0; half < 2; ++half) {
                 const uint32_t lo = half ? __byte_perm(v[0][i], v[1][i], 0x7362) : __byte_perm(v[0][i], v[1][i], 0x5140);
                 const uint32_t hi = half ? __byte_perm(v[2][i], v[3][i], 0x7362) : __byte_perm(v[2][i], v[3][i], 0x5140);
-                const uint32_t a0 = exact_codes<0x4140>(lo), a1 = exact_codes<0x4342>(lo);
-                const uint32_t a2 = exact_codes<0x4140>(hi), a3 = exact_codes<0x4342>(hi);
+                const uint32_t a0 = code_pair<0x4140>(lo), a1 = code_pair<0x4342>(lo);
+                const uint32_t a2 = code_pair<0x4140>(hi), a3 = code_pair<0x4342>(hi);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma16816(acc[2 * i + half][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
             }

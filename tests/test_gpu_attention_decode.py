@@ -270,3 +270,34 @@ def test_binding_refusals():
         f(Q, *cache.args(), scale=float("inf"))
     with pytest.raises(i8.I8RError):
         f(Q, *cache.args(), workspace_buf=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("low", [256, 900])
+@pytest.mark.parametrize("Hq,H,D", [(4, 4, 128), (24, 2, 128), (6, 2, 64), (16, 1, 64)])
+def test_queries_of_nonzero_mean_and_a_channel_that_dominates(Hq, H, D, low):
+    """Scores are sums over q * code, whatever their means: with q = i / 128, i a whole number up to 1000,
+    no partial sum over i * code reaches 128 * 1000 * 127 < 2^24, so that fp32 holds every one exactly.
+    Left are the roundings of the score's factors and of its distance from the maximum (at most 8
+    steps of 2^-23 of the largest score, in numerator and sum), the weights' and the output's 2^-11,
+    and the sums over tokens."""
+    scale, lens = 0.25, [1000, 64, 300, 1]
+    cache = Cache(40 + Hq + D, lens, H, D)
+    g = torch.Generator(device="cuda").manual_seed(low + Hq)
+    K, sK = cache.codes[0], cache.scale[0]
+    K.copy_((6.35 * torch.randn(K.shape, generator=g, device="cuda")).round().clamp(-127, 127))
+    K[..., 3] = torch.randint(115, 128, K.shape[:-1], generator=g, device="cuda")
+    sK.fill_(20.0)
+    Q = (torch.randint(low, 1001, (len(lens), Hq, D), generator=g, device="cuda") / 128).half()
+    O = i8.int8_attention_decode(Q, *cache.args(), scale=scale)
+    G = Hq // H
+    for b, n in enumerate(lens):
+        for h in range(H):
+            k, v = cache.values(b, h)
+            x = scale * Q[b, h * G:(h + 1) * G].double() @ k.T
+            w = torch.softmax(x, 1)
+            o, A = w @ v, w @ v.abs()
+            tol = (o.abs() * 2.0 ** -11 + 2.0 ** -25 + n * 2.0 ** -25 * v.abs().amax() +
+                   A * (2.0 ** -11 + 2 * 8 * 2.0 ** -23 * x.abs().amax(1, keepdim=True) + (n / 16 + 64) * 2.0 ** -23))
+            off = (O[b, h * G:(h + 1) * G].double() - o).abs()
+            assert bool((off <= tol).all()), f"sequence {b}, head {h}: {(off / tol).max().item():.2f} of the tolerance"
+    assert device_status_clean()
