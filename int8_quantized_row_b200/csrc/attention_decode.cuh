@@ -31,10 +31,13 @@
 // subtraction takes the 1152 off again.  (Left in K's operand and taken off the sums
 // instead, it costs fp32 sums of the size of 1152 |sum(Q)|: scores that are 0.001 to
 // 0.003 off where the queries' mean is 3 to 8, and saves nothing: 264 us for 266 on 64
-// long sequences of 12 queries a head.)  p = e^(x - max) <= 1 is rounded to fp16 (2^-11) for the second product,
-// as the output will be, and the softmax's sum is that of the rounded p (one more
-// MMA, with ones for V).  The sums over V are kept in units of the current block's
-// scale, so the MMAs accumulate in place.
+// long sequences of 12 queries a head.)  p = 2^14 e^(x - max) is rounded to fp16 for
+// the second product (2^-11, as the output will be), and the softmax's sum is that of
+// the rounded p (one more MMA, with ones for V).  With 2^14 in front a weight down to
+// 2^-28 of the largest is a normal number and is rounded by 2^-39 of the largest below
+// that: with the largest at 1, weights below 2^-25 were lost, 131072 of which are 0.4 %
+// of the result.  The sums over V are kept in units of the current block's scale, so the
+// MMAs accumulate in place.
 #pragma once
 
 #include "device_common.cuh"
@@ -103,6 +106,14 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two weights in fp16, a in the low half.  Above fp16's largest value they become that (from
+// 2^25 on, a score's rounding exceeds the factor 4 that is left); a NaN stays.
+__device__ __forceinline__ uint32_t weights2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+constexpr float RAISED = 14.0f;          // log2 of what stands in front of the weights
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -339,7 +350,7 @@ __device__ __forceinline__ void issue_q(const DecodeParams &p, const Place &w, u
     }
 }
 
-// One piece of an item in memory: per query its maximum (log2 units), its sum
+// One piece of an item in memory: per query its maximum - RAISED (log2 units), its sum
 // and its D unnormalised values.
 template <int D>
 __device__ __forceinline__ float *piece_row(float *piece, int q) { return piece + q * (D + 2); }
@@ -347,7 +358,7 @@ __device__ __forceinline__ float *piece_row(float *piece, int q) { return piece 
 template <int D, int NT>
 struct State {
     float acc[D / 16][NT][4];            // in units of vs
-    float m[NT][2], l[NT][2];            // of this lane's queries 2t, 2t + 1: the same in all its g
+    float m[NT][2], l[NT][2];            // maximum - RAISED (log2 units) and sum of this lane's queries 2t, 2t + 1: the same in all its g
     float vs;                            // the scale acc is in (sV/127 of the last block with any)
     uint2 q[D / 16][NT];                 // the queries' fragments
 
@@ -456,7 +467,7 @@ struct State {
                 }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const float to = fmaxf(top * ks, m[n][e]);
+                const float to = fmaxf(fmaf(top, ks, -RAISED), m[n][e]);
                 alpha[e] = ex2(m[n][e] - to);
                 m[n][e] = to;
 #pragma unroll
@@ -474,10 +485,8 @@ struct State {
 #pragma unroll
             for (int j = 0; j < SUBS; ++j) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const __half2 h = __floats2half2_rn(x[j >> 1][j & 1][n][2 * r], x[j >> 1][j & 1][n][2 * r + 1]);
-                    pf[j][n][r] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
-                }
+                for (int r = 0; r < 2; ++r)
+                    pf[j][n][r] = transpose8x8(weights2(x[j >> 1][j & 1][n][2 * r], x[j >> 1][j & 1][n][2 * r + 1]));
                 mma16816(sum, kOnes, kOnes, kOnes, kOnes, pf[j][n][0], pf[j][n][1]);
             }
 #pragma unroll

@@ -301,3 +301,53 @@ def test_queries_of_nonzero_mean_and_a_channel_that_dominates(Hq, H, D, low):
             off = (O[b, h * G:(h + 1) * G].double() - o).abs()
             assert bool((off <= tol).all()), f"sequence {b}, head {h}: {(off / tol).max().item():.2f} of the tolerance"
     assert device_status_clean()
+
+
+@pytest.mark.parametrize("below", [24.6, 25.5, 28.0])
+@pytest.mark.parametrize("G", [1, 12])
+def test_one_high_score_over_many_low_ones(G, below):
+    """131072 tokens that each weigh 2^-below of the first: together a tail that fp16 shows.  Weights are
+    rounded with 2^14 in front, so the smallest normal one is 2^-28 of the largest and a rounding among
+    the subnormals at most 2^-39 of it."""
+    n, B, H, D = 131072, 24, 4, 64
+    cache = Cache(50, [n], H, D, spare=0)
+    first = cache.table[0, 0].long()
+    K, V = cache.codes
+    K.zero_()
+    V.fill_(127)
+    K[first, :, 0, 0] = 127
+    V[first, :, 0] = 0
+    for s in cache.scale:
+        s.fill_(127.0)                                       # a code stands for itself
+    table, lengths = cache.table.expand(B, -1).contiguous(), cache.lengths.expand(B).contiguous()
+    Q = torch.zeros(B, H * G, D, dtype=torch.float16, device="cuda")
+    Q[:, :, 0] = 1.0
+    scale = below * np.log(2.0) / 127
+    O = i8.int8_attention_decode(Q, *cache.codes, *cache.scale, table, lengths, scale=scale).double()
+    o = 127 * (n - 1) / (2.0 ** below + n - 1)
+    X = below * np.log(2.0)
+    tol = (2.0 ** -11 * o + 2.0 ** -25 + 127 * n * 2.0 ** -39 +
+           o * (2.0 ** -11 + 2 * 8 * 2.0 ** -23 * X + (n / 16 + 64) * 2.0 ** -23))
+    assert (O - o).abs().max().item() <= tol, f"{(O - o).abs().max().item():.3e} off {o:.3e}, tolerance {tol:.3e}"
+    assert device_status_clean()
+
+
+@pytest.mark.parametrize("G", [1, 12])
+@pytest.mark.parametrize("scale", [0.01, 1.0, 6.0, -6.0])
+def test_scores_whose_rounding_exceeds_the_weights_range(G, scale):
+    """Scores up to 2^28.4 in units of log 2, where fp32 rounds to multiples of 32: the key that is far ahead is
+    the result, whichever way its distance from the maximum is rounded."""
+    n, H, D = 300, 2, 64
+    cache = Cache(60, [n], H, D)
+    cache.scale[0].fill_(65504.0)
+    cache.codes[0].zero_()
+    pages = cache.table[0].long()
+    for t, code in ((77, 127), (205, -127), (276, 100)):
+        cache.codes[0][pages[t // BLOCK], :, t % BLOCK] = code
+    Q = torch.linspace(8, 10, H * G, device="cuda")[None, :, None].expand(1, H * G, D).half().contiguous()
+    O = i8.int8_attention_decode(Q, *cache.args(), scale=scale)
+    for h in range(H):
+        want = cache.values(0, h)[1][77 if scale > 0 else 205]
+        got = O[0, h * G:(h + 1) * G].double()
+        assert bool(((got - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all())
+    assert device_status_clean()
