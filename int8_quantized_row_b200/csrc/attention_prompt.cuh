@@ -19,7 +19,10 @@
 // function units: both pipes have to be kept busy, and neither can go below
 // half of the time.  m_i is only raised (and O rescaled, by the softmax warps)
 // when a row's maximum has grown by more than 2^8: e^(x-m) then stays below 256,
-// which fp16 and the fp32 sums hold as exactly as values below 1.
+// which fp16 and the fp32 sums hold as exactly as values below 1.  P and its sum are
+// 2^7 times that, below 2^15: a weight down to 2^-21 of the reference is a normal fp16
+// number and is rounded by 2^-32 of it below that.  (With 1 at the reference, weights
+// below 2^-25 were lost, 131072 of which are 0.4 % of the result.)
 //
 // What a mask leaves out must not be multiplied by zero: 0 * NaN is NaN.  Scores
 // are replaced, not scaled, and on the one to three steps of a piece that a mask
@@ -57,6 +60,10 @@ constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * 128 <= PROMPT_LAUNCH_REGS * PROMPT_THREADS, "more registers than launched with");
 constexpr uint32_t PROMPT_TMEM = 512;
 constexpr float RAISE = 8.0f;                  // log2 of how far a row may exceed its reference
+// log2 of what stands in front of the weights of a row with this reference (in log2
+// units).  From 2^22 on fp32 rounds a score by 2^-2 and more, which fp16 has no room for
+// beside 2^7 and 2^8.
+__device__ __forceinline__ float raised(float reference) { return fabsf(reference) < 4194304.0f ? 7.0f : 0.0f; }
 
 constexpr int OUT_BYTES = 32 * 128;            // a softmax warp's rows on their way out, 64 columns at a time
 
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 const float mx = fmaxf(max3(max3(top[0], top[1], x(PT - 4)), max3(top[2], top[3], x(PT - 3)), x(PT - 2)), x(PT - 1));
                 if (__any_sync(0xFFFFFFFFu, mx > m + raise)) {
                     const float to = fmaxf(m, mx);
-                    const float alpha = m == -INFINITY ? 0.0f : ex2((m - to) * sl2);
+                    const float alpha = m == -INFINITY ? 0.0f : ex2(fmaf(m - to, sl2, raised(to * sl2) - raised(m * sl2)));
                     l *= alpha;
                     m = to;
                     if (j > 0) {
@@ -616,8 +623,8 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 if (before >= 0 && before < both)
                     ok = ready(&bars->turn[1 - i][quad], (turns + before) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                 if (!ok) break;
-                // p = 2^(x * scale_log2 - m * scale_log2); a row that has seen nothing yet has all -inf
-                const float ref = m == -INFINITY ? 0.0f : -m * sl2;
+                // p = 2^(x * scale_log2 - m * scale_log2 + 7); a row that has seen nothing yet has all -inf
+                const float ref = m == -INFINITY ? 0.0f : fmaf(-m, sl2, raised(m * sl2));
                 const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(ref, ref);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll

@@ -256,3 +256,43 @@ def test_rows_far_apart():
     i8.int8_attention_prompt(*far[:3], cum([n]), O=far[3])
     assert torch.equal(far[3], i8.int8_attention_prompt(Q, K, V, cum([n])))
     assert device_status_clean()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("below", [24.6, 25.5])
+def test_one_high_score_over_many_low_ones(D, below):
+    """131072 keys that each weigh 2^-below of the first: together a tail that fp16 shows.  Weights are
+    rounded with 2^7 in front, so that a rounding among the subnormals is at most 2^-32 of the largest."""
+    nq, n, H = 3, 131072, 2
+    Q, K, V = (torch.zeros(r, H, D, dtype=torch.float16, device="cuda") for r in (nq, n, n))
+    Q[:, :, 0] = 1.0
+    K[0, :, 0] = 32.0
+    V[1:] = 1.0
+    scale = below * np.log(2.0) / 32
+    O = i8.int8_attention_prompt(Q, K, V, cum([nq]), cum([n]), scale=scale).double()
+    low = torch.arange(n - nq, n, device="cuda").double()[:, None, None]                   # a row's other keys
+    o = low / (2.0 ** below + low)
+    X = below * np.log(2.0)
+    tol = (2.0 ** -11 * o + 2.0 ** -25 + n * 2.0 ** -32 +
+           o * (2.0 ** -11 + 2 * 8 * 2.0 ** -23 * X + (n / 8 + 64) * 2.0 ** -23))
+    off = (O - o).abs()
+    assert bool((off <= tol).all()), f"{off.max().item():.3e} off {o.max().item():.3e}, tolerance {tol.max().item():.3e}"
+    assert device_status_clean()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, 100.0, -100.0])
+def test_scores_whose_rounding_nears_the_weights_range(D, scale):
+    """Scores up to 2^26 in units of log 2, which fp32 rounds to multiples of 4, first those below 2^22: the
+    keys that are far ahead of those before them are the result, one after the other."""
+    n = 700
+    Q, K, V = (torch.zeros(n, 1, D, dtype=torch.float16, device="cuda") for _ in range(3))
+    V.copy_(inputs(17, [n], [n], 1, 1, D)[2])
+    Q[:, 0, :8] = torch.linspace(90, 100, n, device="cuda")[:, None].half()
+    for key, x in ((3, 8.0), (200, 300.0), (450, 600.0)):          # 100 * 600 * 8 * 100 = 2^25.5
+        K[key, 0, :8] = x if scale > 0 else -x
+    O = i8.int8_attention_prompt(Q, K, V, cum([n]), scale=scale)
+    for a, e, key in ((3, 200, 3), (200, 450, 200), (450, n, 450)):
+        want = V[key].double()
+        assert bool(((O[a:e].double() - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all()), key
+    assert device_status_clean()
