@@ -296,3 +296,31 @@ def test_scores_whose_rounding_nears_the_weights_range(D, scale):
         want = V[key].double()
         assert bool(((O[a:e].double() - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all()), key
     assert device_status_clean()
+
+
+def test_a_long_prefix_beside_many_short_prompts():
+    """The search for work passes over lengths that no sequence has: 2^20 cached keys of one row (4096
+    lengths, in 256 keys) beside 4000 short prompts take little longer than the two apart."""
+    B, far, D = 4000, 1 << 20, 64
+    n = [1 + b % 5 for b in range(B)]
+    Q, K, V = inputs(16, [1, *n], [far, *n], 1, 1, D)
+    calls = {"long": (Q[:1], K[:far], V[:far], cum([1]), cum([far])),
+             "short": (Q[1:], K[far:], V[far:], cum(n), cum(n)),
+             "both": (Q, K, V, cum([1, *n]), cum([far, *n]))}
+    ms, out = {}, {}
+    for name, args in calls.items():
+        O = torch.empty_like(args[0])
+        times = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            i8.int8_attention_prompt(*args, O=O)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        ms[name], out[name] = min(times[1:]), O
+    assert torch.equal(out["both"], torch.cat([out["long"], out["short"]]))
+    check(out["short"], *calls["short"][:3], n, n, D ** -0.5)
+    check(out["long"], *calls["long"][:3], [1], [far], D ** -0.5)
+    assert ms["both"] <= 3 * (ms["long"] + ms["short"]), ms
+    assert device_status_clean()
