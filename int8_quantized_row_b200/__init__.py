@@ -143,6 +143,17 @@ def _dev(t, dtype, name, ndim=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _buffer(t):
+    """Address and bytes of a workspace: a contiguous CUDA tensor of any type (what a strided
+    one counts as its bytes lies in several places)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("workspace_buf must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace_buf must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+
+
 # Argument checks of the decoder layer's operators.  They are on the path of every
 # token, so they ask a tensor for as little as they can (about 0.1 us a question)
 # and hand plain integers to ctypes.
@@ -231,8 +242,14 @@ def _workspace(workspace_buf, size, device, like):
     """A buffer of `size` bytes where `like` is, and its address and bytes; or the caller's."""
     if workspace_buf is None:
         workspace_buf = like.new_empty(max(1, size), dtype=torch.uint8)
-    elif workspace_buf.get_device() != device:
-        _wrong(workspace_buf, "workspace_buf", device, workspace_buf.dtype)
+    else:
+        try:
+            if workspace_buf.get_device() != device:
+                _wrong(workspace_buf, "workspace_buf", device, workspace_buf.dtype)
+        except AttributeError:
+            _wrong(workspace_buf, "workspace_buf", device, None)
+        if not workspace_buf.is_contiguous():
+            raise ValueError("workspace_buf must be contiguous")
     return workspace_buf, workspace_buf.data_ptr(), workspace_buf.numel() * workspace_buf.element_size()
 
 
@@ -268,7 +285,7 @@ def int8_mixed_linear(X, Wq, sW, W16, alpha=6.0, Y=None, workspace_buf=None, str
     _check("int8_mixed_linear", lib().int8_mixed_linear(
         _dev(X, torch.float16, "X", 2), T, K, _dev(Wq, torch.int8, "Wq", 2), _dev(sW, torch.float32, "sW"),
         _dev(W16, torch.float16, "W16", 2), N, float(alpha), _dev(Y, torch.float16, "Y"),
-        ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)))
+        *_buffer(ws), _stream(stream)))
     return Y
 
 
@@ -293,7 +310,7 @@ def int8_mixed_linear_wq(X, Wq, sW, alpha=6.0, Y=None, workspace_buf=None, strea
     _check("int8_mixed_linear_wq", lib().int8_mixed_linear_wq(
         _dev(X, torch.float16, "X", 2), T, K, _dev(Wq, torch.int8, "Wq", 2), _dev(sW, torch.float32, "sW"),
         N, float(alpha), _dev(Y, torch.float16, "Y"),
-        ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)))
+        *_buffer(ws), _stream(stream)))
     return Y
 
 
@@ -359,8 +376,7 @@ def int8_mixed_linear_chain(layers, workspace_buf=None, stream=None):
         dev = layers[0][0].device if layers else "cuda"
         workspace_buf = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
     _check("int8_mixed_linear_chain", lib().int8_mixed_linear_chain(
-        len(layers), ctypes.cast(arr, _P), ctypes.c_void_p(workspace_buf.data_ptr()),
-        workspace_buf.numel() * workspace_buf.element_size(), _stream(stream)))
+        len(layers), ctypes.cast(arr, _P), *_buffer(workspace_buf), _stream(stream)))
     return outs
 
 
@@ -512,8 +528,7 @@ def int4_linear(X, W4, S4, N, Y=None, workspace_buf=None, stream=None):
     ws = workspace_buf
     _check("int4_linear", lib().int4_linear(
         _dev(X, torch.float16, "X", 2), T, K, _dev(W4, torch.uint8, "W4"), _dev(S4, torch.uint8, "S4"), int(N),
-        _dev(Y, torch.float16, "Y"), ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        _dev(Y, torch.float16, "Y"), *_buffer(ws), _stream(stream)))
     return Y
 
 

@@ -252,3 +252,35 @@ def test_two_streams_at_once():
     for a, b in zip(got[0] + got[1], want[0] + want[1]):
         assert torch.equal(a, b)
     assert device_status_clean()
+
+
+def test_workspaces_that_are_no_buffer_are_refused():
+    """A strided view counts bytes that are not its own; each call refuses it before any kernel runs."""
+    T, K, N = 4, 256, 256
+    x, w = torch.randn(T, K, device="cuda").half(), torch.randn(K, N, device="cuda").half()
+    Wq, sW = i8.int8_quantize_weight_colwise(w)
+    W4, S4 = i8.int4_quantize_weight_groupwise(w)
+    codes = [torch.zeros(2, 1, 64, 64, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.ones(2, 1, device="cuda") for _ in range(2)]
+    table, lengths = (torch.ones(n, dtype=torch.int32, device="cuda") for n in ((1, 1), (1,)))
+    y = torch.empty(T, N, dtype=torch.float16, device="cuda")
+    calls = [lambda ws: i8.int8_mixed_linear(x, Wq, sW, w, workspace_buf=ws),
+             lambda ws: i8.int8_mixed_linear_wq(x, Wq, sW, workspace_buf=ws),
+             lambda ws: i8.int8_mixed_linear_fused(x, Wq, sW, w, workspace_buf=ws),
+             lambda ws: i8.int8_mixed_linear_fused(x, Wq, sW, workspace_buf=ws),
+             lambda ws: i8.int8_mixed_linear_chain([(x, Wq, sW, w, 6.0, y)], workspace_buf=ws),
+             lambda ws: i8.int4_linear(x, W4, S4, N, workspace_buf=ws),
+             lambda ws: i8.int8_attention_decode(x[:1, :64].view(1, 1, 64), *codes, *scale, table, lengths,
+                                                 workspace_buf=ws)]
+    size = 64 << 20
+    buf = torch.empty(2, size, dtype=torch.uint8, device="cuda")
+    for call in calls:
+        for strided in (buf.view(size, 2)[:, 0], buf[:1, ::2], buf[:, :size // 2]):
+            with pytest.raises(ValueError):
+                call(strided)
+        for other in (torch.empty(size, dtype=torch.uint8), 4096):
+            with pytest.raises(TypeError):
+                call(other)
+        call(buf)                                                  # any shape and type will do
+        call(buf[1].view(torch.float32))
+    assert device_status_clean()
