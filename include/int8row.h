@@ -326,6 +326,8 @@ void int4_debug_set_product_path(int mode);
  * Rows are expected finite.  A NaN or an infinity among a block's rows makes
  * its scale NaN or infinite, which shows in all the block's values of that head.
  *
+ * The int32 arrays and the scales need 4-byte alignment only, here and in the
+ * attention calls below.
  * The int32 arrays are read on the device.  A length, row range or block number
  * out of range is skipped and reported as I8R_DEV_BAD_INDEX in the device status
  * word (rows that it belongs to are undefined); nothing out of bounds is

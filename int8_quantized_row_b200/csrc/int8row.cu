@@ -272,7 +272,8 @@ i8r_status check_ptr(const void *p) {
 }
 
 
-i8r_status check_index_ptr(const int32_t *p) {
+// An array that is read one 32-bit word at a time: counts, block numbers, a cache's scales.
+i8r_status check_words_ptr(const void *p) {
     if (!p) return I8R_EINVAL;
     return (reinterpret_cast<uintptr_t>(p) & 3u) ? I8R_EALIGN : I8R_OK;
 }
@@ -729,16 +730,17 @@ i8r_status check_ld(long long ld, int H, int D) {
     return ld % 8 ? I8R_EALIGN : I8R_OK;
 }
 
-// The cache's own arguments (int32 arrays need 4-byte alignment only).
+// The cache's own arguments.  Scales need no more than their own alignment: they may be
+// a layer's part of a larger tensor.
 i8r_status check_cache(const void *Kc, const void *Vc, const void *sK, const void *sV, int num_blocks,
                        const int32_t *block_table, int max_blocks) {
     if (num_blocks < 0 || max_blocks < 0) return I8R_EINVAL;
     if (num_blocks == 0 || max_blocks == 0) return I8R_ERANGE;
     I8R_TRY(check_ptr(Kc));
     I8R_TRY(check_ptr(Vc));
-    I8R_TRY(check_ptr(sK));
-    I8R_TRY(check_ptr(sV));
-    return check_index_ptr(block_table);
+    I8R_TRY(check_words_ptr(sK));
+    I8R_TRY(check_words_ptr(sV));
+    return check_words_ptr(block_table);
 }
 
 // Query heads: a multiple of the key/value heads.
@@ -1237,8 +1239,8 @@ i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long
     if (n_new == 0 || B == 0) return I8R_OK;
     I8R_TRY(check_ptr(K));
     I8R_TRY(check_ptr(V));
-    I8R_TRY(check_index_ptr(cu_new));
-    I8R_TRY(check_index_ptr(past));
+    I8R_TRY(check_words_ptr(cu_new));
+    I8R_TRY(check_words_ptr(past));
     I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
     const DeviceInfo *dev = nullptr;
     I8R_TRY(device_setup(&dev));
@@ -1289,7 +1291,7 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
     if (rows == 0 || B == 0) return I8R_OK;
     I8R_TRY(check_ptr(K));
     I8R_TRY(check_ptr(V));
-    I8R_TRY(check_index_ptr(cu));
+    I8R_TRY(check_words_ptr(cu));
     I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
     const DeviceInfo *dev = nullptr;
     I8R_TRY(device_setup(&dev));
@@ -1329,7 +1331,7 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     if (B == 0) return I8R_OK;
     I8R_TRY(check_ptr(Q));
     I8R_TRY(check_ptr(O));
-    I8R_TRY(check_index_ptr(lengths));
+    I8R_TRY(check_words_ptr(lengths));
     I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
     if (static_cast<long long>(num_blocks) * H > 0x7FFFFFFFll) return I8R_ERANGE;
     if (!workspace || workspace_bytes < int8_attention_decode_workspace_size(Hq, H, D)) return I8R_EWORKSPACE;
@@ -1374,8 +1376,8 @@ i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, lo
         I8R_TRY(check_ptr(K));
         I8R_TRY(check_ptr(V));
     }
-    I8R_TRY(check_index_ptr(cu_q));
-    I8R_TRY(check_index_ptr(cu_k));
+    I8R_TRY(check_words_ptr(cu_q));
+    I8R_TRY(check_words_ptr(cu_k));
     // tiles of 256 rows: at most one part-filled tile a sequence, and none without a row
     const long long tiles = std::min<long long>(N, (N + (attn::PROMPT_ROWS - 1ll) * B) / attn::PROMPT_ROWS);
     if (tiles * Hq > 0x7FFFFFFFll) return I8R_ERANGE;

@@ -144,3 +144,21 @@ def test_prompt_attention_refusals(so):
     assert call(N=1 << 30, B=1, Hq=8192, H=8192, ldq=1 << 20, ldk=1 << 20, ldv=1 << 20, ldo=1 << 20) == ERANGE
     assert call(N=0, q=NULL) == OK
     assert call(B=0, q=NULL) == OK
+
+
+def test_scales_and_counts_need_word_alignment_only(so):
+    """A layer's scales may begin anywhere in a stacked tensor.  (Without a GPU the calls end at the
+    device's setup, after the checks.)"""
+    size = so.int8_attention_decode_workspace_size(4, 2, 128)
+
+    def calls(sk=p(), sv=p(), words=p()):
+        yield so.int8_kv_append(p(), 256, p(), 256, 4, 2, 128, words, words, 2, p(), p(), sk, sv, 9, words, 3, NULL)
+        yield so.int8_kv_gather(p(), p(), sk, sv, 9, 2, 128, words, 3, words, 2, 4, p(), p(), NULL)
+        yield so.int8_attention_decode(p(), 512, 2, 4, 2, 128, p(), p(), sk, sv, 9, words, 3, words, 0.1, p(), 512, p(),
+                                       size, NULL)
+
+    import torch
+    if not torch.cuda.is_available():                       # (no call may get as far as a launch)
+        assert set(calls(p(4100), p(4108), p(4104))) <= {5, 7}
+    for bad in (dict(sk=p(4098)), dict(sv=p(4097)), dict(words=p(4099))):
+        assert set(calls(**bad)) == {EALIGN}

@@ -284,3 +284,24 @@ def test_workspaces_that_are_no_buffer_are_refused():
         call(buf)                                                  # any shape and type will do
         call(buf[1].view(torch.float32))
     assert device_status_clean()
+
+
+def test_scales_of_a_layer_in_a_stacked_tensor():
+    """Codes and scales of several layers in one tensor, with a layer's scales at an odd word."""
+    layers, blocks, H, D = 3, 5, 3, 64
+    codes = [torch.zeros(layers, blocks, H, 64, D, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.full((layers, blocks, H), 7.0, device="cuda") for _ in range(2)]
+    x = [torch.randn(200, H, D, device="cuda").half() for _ in range(3)]
+    table = torch.tensor([[4, 1, 3, 0]], dtype=torch.int32, device="cuda")
+    one = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    outs = []
+    for i in range(layers):
+        assert scale[0][i].data_ptr() % 16 == 60 * i % 16
+        cache = (codes[0][i], codes[1][i], scale[0][i], scale[1][i])
+        i8.int8_kv_append(x[0], x[1], one(0, 200), one(0), table, *cache)
+        outs.append((*i8.int8_kv_gather(*cache, one(0, 200), table, 200),
+                     i8.int8_attention_decode(x[2][:1], *cache, table, one(200))))
+    for out in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out, outs[0]))
+    assert (scale[0][:, 2] == 7.0).all() and (scale[1][:, 2] == 7.0).all()      # the block that no sequence has
+    assert device_status_clean()
