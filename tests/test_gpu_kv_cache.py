@@ -323,3 +323,38 @@ def test_offsets_past_32_bits():
     for a, b in zip(near, far):
         assert torch.equal(a, b)
     assert device_status_clean()
+
+
+def holds(s, codes, scale):
+    """Codes and scales of the cache, bit for bit, after s was appended."""
+    for c, sc, w in zip(codes, scale, s.want()):
+        assert np.array_equal(sc.cpu().numpy().astype(np.float64), w.scale)
+        assert np.array_equal(c.cpu().numpy(), w.codes.astype(np.int8))
+    assert device_status_clean()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("offset,rows", [(5, 64), (0, 64), (63, 70), (1, 9), (40, 100)])
+@pytest.mark.parametrize("grow", [0.2, 8.0])
+def test_a_longer_row_range_among_single_tokens(D, offset, rows, grow):
+    """At most 8 new rows a sequence on average: one warp a block and head, also where a block gets more rows
+    than the warp holds (those are read twice), with scales that stay and scales that grow."""
+    past = [(37 * b + 3) % 130 for b in range(16)]
+    new = [b % 2 for b in range(16)]
+    past[6], new[6] = 128 + offset, rows
+    s = Setup(30 + rows, past, new, 3, D)
+    for x in s.x:
+        x *= np.float16(grow)
+        x[s.cu[6] + rows - 1] *= np.float16(4)             # the largest in the last row
+    codes, scale = s.device()
+    s.append(codes, scale)
+    holds(s, codes, scale)
+
+
+@pytest.mark.parametrize("B,H,D", [(128, 96, 64), (120, 96, 128), (700, 9, 128), (700, 40, 64), (1100, 40, 64)])
+def test_single_tokens_of_more_heads_than_a_pass_covers(B, H, D):
+    """A block's CTA goes on to further heads, found by a warp (up to 128 sequences) or by the CTA."""
+    s = Setup(31 + B, [(29 * b) % 64 for b in range(B)], [1] * B, H, D, spare=1)
+    codes, scale = s.device()
+    s.append(codes, scale)
+    holds(s, codes, scale)
