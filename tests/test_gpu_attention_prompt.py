@@ -281,20 +281,40 @@ def test_one_high_score_over_many_low_ones(D, below):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("scale", [1.0, 100.0, -100.0])
-def test_scores_whose_rounding_nears_the_weights_range(D, scale):
-    """Scores up to 2^26 in units of log 2, which fp32 rounds to multiples of 4, first those below 2^22: the
-    keys that are far ahead of those before them are the result, one after the other."""
-    n = 700
-    Q, K, V = (torch.zeros(n, 1, D, dtype=torch.float16, device="cuda") for _ in range(3))
-    V.copy_(inputs(17, [n], [n], 1, 1, D)[2])
-    Q[:, 0, :8] = torch.linspace(90, 100, n, device="cuda")[:, None].half()
-    for key, x in ((3, 8.0), (200, 300.0), (450, 600.0)):          # 100 * 600 * 8 * 100 = 2^25.5
-        K[key, 0, :8] = x if scale > 0 else -x
-    O = i8.int8_attention_prompt(Q, K, V, cum([n]), scale=scale)
-    for a, e, key in ((3, 200, 3), (200, 450, 200), (450, n, 450)):
-        want = V[key].double()
-        assert bool(((O[a:e].double() - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all()), key
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_infinite_keys_that_a_row_sees(D, bad):
+    """A score of +inf makes its row NaN; a key whose score is -inf weighs nothing."""
+    nq, nk, scale = [200, 300, 100], [260, 300, 90], D ** -0.5
+    Q, K, V = inputs(10, nq, nk, 4, 2, D)
+    at = [150, 260 + 10, 260 + 200, 260 + 299, 560 + 20]
+    worse = K.clone()
+    worse[at, 0, 3] = bad
+    got = i8.int8_attention_prompt(Q, worse, V, cum(nq), cum(nk)).double()
+    nan = never = 0
+    a = c = 0
+    for n, m in zip(nq, nk):
+        live = torch.ones(n, m, device="cuda").tril(m - n).bool()
+        for h in range(2):                                         # the query heads of key/value head 0
+            q, k, v = Q[a:a + n, h].double(), K[c:c + m, 0].double(), V[c:c + m, 0].double()
+            x = torch.where(live, scale * q @ k.T, -torch.inf)
+            for key in at:
+                if c <= key < c + m:
+                    x[:, key - c] = torch.where(live[:, key - c], q[:, 3] * bad, -torch.inf)
+            if m < n:
+                assert (got[a:a + n - m, h] == 0).all()
+            rows = slice(max(0, n - m), n)
+            w = torch.softmax(x[rows], 1)                          # NaN in a row with +inf
+            X = scale * torch.where(live[rows], q[rows].abs() @ k.abs().T, 0.0).amax(1, keepdim=True)
+            y, A = w @ v, w @ v.abs()
+            tol = (y.abs() * 2.0 ** -11 + 2.0 ** -25 + m * 2.0 ** -25 * v.abs().amax() +
+                   A * (2.0 ** -11 + 2 * (D + 8) * 2.0 ** -23 * X + (m / 8 + 64) * 2.0 ** -23))
+            z = got[a:a + n, h][rows]
+            lost = torch.isnan(y)
+            assert torch.equal(torch.isnan(z), lost)
+            assert bool(((z - y).abs() <= tol)[~lost].all())
+            nan, never = nan + lost.any(1).sum().item(), never + (~lost).any(1).sum().item()
+        a, c = a + n, c + m
+    assert nan > 50 and never > 50
     assert device_status_clean()
 
 
@@ -323,4 +343,22 @@ def test_a_long_prefix_beside_many_short_prompts():
     check(out["short"], *calls["short"][:3], n, n, D ** -0.5)
     check(out["long"], *calls["long"][:3], [1], [far], D ** -0.5)
     assert ms["both"] <= 3 * (ms["long"] + ms["short"]), ms
+    assert device_status_clean()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, 100.0, -100.0])
+def test_scores_whose_rounding_nears_the_weights_range(D, scale):
+    """Scores up to 2^26 in units of log 2, which fp32 rounds to multiples of 4, first those below 2^22: the
+    keys that are far ahead of those before them are the result, one after the other."""
+    n = 700
+    Q, K, V = (torch.zeros(n, 1, D, dtype=torch.float16, device="cuda") for _ in range(3))
+    V.copy_(inputs(17, [n], [n], 1, 1, D)[2])
+    Q[:, 0, :8] = torch.linspace(90, 100, n, device="cuda")[:, None].half()
+    for key, x in ((3, 8.0), (200, 300.0), (450, 600.0)):          # 100 * 600 * 8 * 100 = 2^25.5
+        K[key, 0, :8] = x if scale > 0 else -x
+    O = i8.int8_attention_prompt(Q, K, V, cum([n]), scale=scale)
+    for a, e, key in ((3, 200, 3), (200, 450, 200), (450, n, 450)):
+        want = V[key].double()
+        assert bool(((O[a:e].double() - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all()), key
     assert device_status_clean()
