@@ -213,11 +213,12 @@ struct Order {
         share = total / warps;
         rest = static_cast<int>(total - share * warps);
     }
-    // The first block of warp w's range, floor(total * w / warps), and the warp whose range holds block u.
+    // The first block of warp w's range, floor(total * w / warps), and the warp whose range holds
+    // block u < total (so total > 0).
     __device__ __forceinline__ long long begin(int w) const {
         return share * w + static_cast<unsigned>(rest * w) / static_cast<unsigned>(warps);
     }
-    __device__ __forceinline__ int owner(long long u) const {
+    __device__ __forceinline__ static int owner(long long u, int warps, long long total) {
         return static_cast<int>(((u + 1) * warps - 1) / total);
     }
     // Block u < total.
@@ -747,8 +748,7 @@ __global__ void __launch_bounds__(32 * dec_warps(NT), 1)
         const int out_slot = a.front ? 0 : 1;
         // an item that goes on in other CTAs (the last one here, if any)
         if (a.starts && pieces[last].left > 0 && threadIdx.x == 0) {
-            const long long end = cta_end + pieces[last].left - 1;
-            const int ends_in = static_cast<int>(((end + 1) * (gridDim.x * cta_warps) - 1) / total) / cta_warps;
+            const int ends_in = Order::owner(cta_end + pieces[last].left - 1, gridDim.x * cta_warps, total) / cta_warps;
             p.joins[blockIdx.x] = Join{a.b, a.h, a.gt, out_slot, ends_in, 1};
             joined = true;
         }

@@ -21,7 +21,7 @@ namespace i8r {
 namespace kv {
 
 constexpr int BLOCK = 64;            // tokens per cache block
-constexpr int WARPS = 8;             // warps per CTA: one (head, K or V) each
+constexpr int WARPS = 8;             // warps per CTA: a (head, K or V) is one's or, appending prompts, four warps'
 
 struct Cache {
     int8_t *codes[2];                // K, V: [num_blocks, H, BLOCK, D]
