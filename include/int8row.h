@@ -369,6 +369,8 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
  *   Hq       query heads, a multiple of the H key/value heads
  *   lengths  [B] int32: tokens of each sequence in the cache, the new one
  *            included; 0 gives a row of zeros
+ *   num_blocks  below 2^31 / H; min(max_blocks, 2^25) up to 2^32 / (H * ceil(Hq / H / 16)),
+ *            which it always is for up to 128 of those
  *   scale    finite; usually 1 / sqrt(D)
  *   workspace  int8_attention_decode_workspace_size(Hq, H, D) bytes, 256-byte
  *            aligned; its contents on entry are ignored.  Two calls that share a

@@ -243,7 +243,7 @@ struct Order {
                     if (k == j && r >= c) r -= c, k = j + 1;
                 }
                 const int own = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
-                // within one sequence: at most 2^31 blocks, as the cache has (32-bit slots)
+                // within one sequence: H * GT * max_blocks at most, which the host checks
                 const unsigned in = static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, r, at));
                 w->len = __shfl_sync(0xFFFFFFFFu, own, at);
                 w->b = __shfl_sync(0xFFFFFFFFu, b0 + 4 * lane + k, at);

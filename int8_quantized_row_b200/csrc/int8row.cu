@@ -1334,11 +1334,13 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     I8R_TRY(check_words_ptr(lengths));
     I8R_TRY(check_cache(Kc, Vc, sK, sV, num_blocks, block_table, max_blocks));
     if (static_cast<long long>(num_blocks) * H > 0x7FFFFFFFll) return I8R_ERANGE;
+    // the blocks of one sequence's items are counted in 32 bits (Order::find); a length, 31 bits, has at most 2^25
+    const DecodeTiles q(Hq, H);
+    if (std::min<long long>(max_blocks, 1ll << 25) * H * q.GT > 1ll << 32) return I8R_ERANGE;
     if (!workspace || workspace_bytes < int8_attention_decode_workspace_size(Hq, H, D)) return I8R_EWORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return I8R_EALIGN;
     const DeviceInfo *dev = nullptr;
     I8R_TRY(device_setup(&dev));
-    const DecodeTiles q(Hq, H);
     attn::DecodeParams p{};
     p.c = make_cache(Kc, Vc, sK, sV, num_blocks, H, D, block_table, max_blocks);
     p.Q = static_cast<const __half *>(Q);

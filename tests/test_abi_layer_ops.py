@@ -162,3 +162,19 @@ def test_scales_and_counts_need_word_alignment_only(so):
         assert set(calls(p(4100), p(4108), p(4104))) <= {5, 7}
     for bad in (dict(sk=p(4098)), dict(sv=p(4097)), dict(words=p(4099))):
         assert set(calls(**bad)) == {EALIGN}
+
+
+def test_decode_attention_counts_a_sequence_in_32_bits(so):
+    """The blocks of one sequence, over all its heads and tiles of 16 query heads, are at most 2^32."""
+    size = so.int8_attention_decode_workspace_size
+
+    def call(Hq, H, blocks, wide, words=p()):
+        return so.int8_attention_decode(p(), Hq * 64, 2, Hq, H, 64, p(), p(), p(), p(), blocks, words, wide, words, 0.1, p(),
+                                        Hq * 64, p(), size(Hq, H, 64) - 1, NULL)
+
+    assert call(8192, 1, 9, (1 << 23) + 1) == ERANGE               # 512 tiles of 2^23 blocks
+    assert call(8192, 1, 9, 1 << 23) == EWORKSPACE                 # (the next check)
+    assert call(129, 129, 9, 1 << 30) == ERANGE                    # a length has 2^25 blocks at most
+    assert call(128, 128, 9, (1 << 31) - 1) == EWORKSPACE
+    assert call(8, 8, 1 << 28, 9) == ERANGE
+    assert call(8, 8, (1 << 28) - 1, 9) == EWORKSPACE
