@@ -371,7 +371,7 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
  *            included; 0 gives a row of zeros
  *   num_blocks  below 2^31 / H; min(max_blocks, 2^25) up to 2^32 / (H * ceil(Hq / H / 16)),
  *            which it always is for up to 128 of those
- *   scale    finite; usually 1 / sqrt(D)
+ *   scale    |scale| * log2(e) is finite; usually 1 / sqrt(D)
  *   workspace  int8_attention_decode_workspace_size(Hq, H, D) bytes, 256-byte
  *            aligned; its contents on entry are ignored.  Two calls that share a
  *            workspace must not overlap on the GPU.
@@ -407,7 +407,7 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
  *          the inputs
  *   D      64 or 128; Hq a multiple of H
  *   cu_q, cu_k [B+1] int32, cumulative, on the device
- *   scale  finite; usually 1 / sqrt(D)
+ *   scale  |scale| * log2(e) is finite; usually 1 / sqrt(D)
  * Keys and values that a row does not see have no effect on it, infinities and
  * NaN included.  Rows of O that belong to no sequence are not touched.  A row
  * range that is out of order or past N or M is reported as I8R_DEV_BAD_INDEX and

@@ -751,6 +751,10 @@ i8r_status check_groups(int Hq, int H, int D) {
     return I8R_OK;
 }
 
+// |scale| in units of log 2, in which the kernels take exponentials: finite too.
+constexpr float kLog2e = 1.44269504088896340736f;
+i8r_status check_scale(float scale) { return std::isfinite(std::fabs(scale) * kLog2e) ? I8R_OK : I8R_EINVAL; }
+
 // How int8_attention_decode cuts a key/value head's queries: into tiles of at
 // most 16, as even as they come (a tile reads the head's codes once).
 struct DecodeTiles {
@@ -1325,7 +1329,8 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
                                  const int32_t *block_table, int max_blocks, const int32_t *lengths, float scale,
                                  void *O, long long ldo, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     I8R_TRY(check_groups(Hq, H, D));
-    if (B < 0 || !std::isfinite(scale)) return I8R_EINVAL;
+    if (B < 0) return I8R_EINVAL;
+    I8R_TRY(check_scale(scale));
     I8R_TRY(check_ld(ldq, Hq, D));
     I8R_TRY(check_ld(ldo, Hq, D));
     if (B == 0) return I8R_OK;
@@ -1352,7 +1357,7 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
     p.G = q.G;
     p.GT = q.GT;
     p.tile = q.tile;
-    p.scale_log2 = std::fabs(scale) * 1.44269504088896340736f;      // log2(e)
+    p.scale_log2 = std::fabs(scale) * kLog2e;
     p.negate = scale < 0.0f ? 0x80008000u : 0u;
     p.part = static_cast<float *>(workspace);
     const size_t piece = static_cast<size_t>(attn::piece_floats(q.tile, D));
@@ -1366,7 +1371,8 @@ i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, lo
                                  const int32_t *cu_k, int B, float scale, void *O, long long ldo,
                                  cudaStream_t stream) {
     I8R_TRY(check_groups(Hq, H, D));
-    if (N < 0 || M < 0 || B < 0 || !std::isfinite(scale)) return I8R_EINVAL;
+    if (N < 0 || M < 0 || B < 0) return I8R_EINVAL;
+    I8R_TRY(check_scale(scale));
     I8R_TRY(check_ld(ldq, Hq, D));
     I8R_TRY(check_ld(ldk, H, D));
     I8R_TRY(check_ld(ldv, H, D));
@@ -1405,7 +1411,7 @@ i8r_status int8_attention_prompt(const void *Q, long long ldq, const void *K, lo
     p.cu_k = cu_k;
     // a negative scale negates the scores in the MMA, and 0 becomes a scale that
     // leaves every finite score at 0 (infinities, the masked places, stay)
-    p.scale_log2 = std::max(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
+    p.scale_log2 = std::max(std::fabs(scale) * kLog2e, 1e-30f);
     p.negate = scale < 0.0f ? 1u << 13 : 0u;
     const dim3 grid(static_cast<unsigned>(std::min<long long>(tiles * Hq, dev->sms)));      // one CTA an SM
     if (D == 128)

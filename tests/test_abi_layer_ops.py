@@ -178,3 +178,18 @@ def test_decode_attention_counts_a_sequence_in_32_bits(so):
     assert call(128, 128, 9, (1 << 31) - 1) == EWORKSPACE
     assert call(8, 8, 1 << 28, 9) == ERANGE
     assert call(8, 8, (1 << 28) - 1, 9) == EWORKSPACE
+
+
+def test_scales_that_overflow_in_units_of_log_2_are_refused(so):
+    """Scores are taken times log2(e): 3e38 times that is no fp32 number.  (B = 0: nothing to do after the checks.)"""
+    def decode(scale):
+        return so.int8_attention_decode(NULL, 512, 0, 4, 2, 128, NULL, NULL, NULL, NULL, 9, NULL, 3, NULL, scale, NULL,
+                                        512, NULL, 0, NULL)
+
+    def prompt(scale):
+        return so.int8_attention_prompt(NULL, 512, NULL, 256, NULL, 256, 9, 9, 4, 2, 128, NULL, NULL, 0, scale, NULL, 512,
+                                        NULL)
+
+    for f in (decode, prompt):
+        assert f(3e38) == EINVAL and f(-3e38) == EINVAL
+        assert f(2e38) == OK and f(-2e38) == OK
