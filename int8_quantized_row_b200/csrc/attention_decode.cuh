@@ -444,7 +444,9 @@ struct State {
     __device__ __forceinline__ void weigh(const DecodeParams &p, float (&x)[SUBS / 2][2][NT][4], float sk, float sv, int hi,
                                           uint32_t (&pf)[SUBS][NT][2]) {
         const int g = (threadIdx.x & 31) >> 2;
-        const float ks = p.scale_log2 * (sk * (1.0f / 127.0f)), now = sv * (1.0f / 127.0f);
+        // s/127 as a product (2^-24 more than the division); an infinite sK makes every score NaN, not
+        // only those of codes whose sum is not negative: a code of 0 stands for NaN then
+        const float ks = fmaf(sk, 0.0f, p.scale_log2 * (sk * (1.0f / 127.0f))), now = sv * (1.0f / 127.0f);
         // a block whose scale is 0 stands for zeros, whatever its codes: values() is not called for it
         const bool nothing = now == 0.0f;
         const float turn = nothing ? 1.0f : vs / now;

@@ -351,3 +351,46 @@ def test_scores_whose_rounding_exceeds_the_weights_range(G, scale):
         got = O[0, h * G:(h + 1) * G].double()
         assert bool(((got - want).abs() <= want.abs() * 2.0 ** -10 + 2.0 ** -24).all())
     assert device_status_clean()
+
+
+@pytest.mark.parametrize("G,D", [(1, 64), (2, 128), (12, 128)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_block_whose_scale_is_not_finite_shows(G, D, bad, which):
+    """Its codes stand for infinities (of both signs) and, where they are 0, NaN: no row that sees them is finite,
+    the others are as before."""
+    lens, H = [300, 64, 30, 700], 4
+    cache = Cache(61 + D, lens, H, D)
+    Q = queries(62, len(lens), H * G, D)
+    want = i8.int8_attention_decode(Q, *cache.args(), scale=0.05)
+    for b, block in ((0, 2), (1, 0), (3, 5)):
+        cache.scale[which][cache.table[b, block].long(), b] = bad              # of head b
+        cache.codes[which][cache.table[b, block].long(), b, :, ::7] = 0
+    got = i8.int8_attention_decode(Q, *cache.args(), scale=0.05)
+    for b in (0, 1, 3):
+        rows = got[b, b * G:(b + 1) * G]
+        seen = rows if which == 0 else rows[:, ::7]                            # (a column of V's own)
+        assert torch.isnan(seen).all()
+        assert not torch.isfinite(rows).any()
+        got[b, b * G:(b + 1) * G] = want[b, b * G:(b + 1) * G]
+    assert torch.equal(got, want)
+    assert device_status_clean()
+
+
+@pytest.mark.parametrize("G", [1, 12])
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_infinite_key_alone_in_its_block(G, D):
+    """Token 128's key holds an infinity: its block's other codes are 0, which stand for NaN, whatever the sign of
+    the query where the infinity is, and whether its warp has the blocks before it or not."""
+    H, n, B = 2, 129, 1200
+    cache = Cache(63, [n] * B, H, D)
+    x = [torch.randn(B, H, D, device="cuda").half() for _ in range(2)]
+    x[0][:, 0, 5] = float("inf")
+    i8.int8_kv_append(*x, torch.arange(B + 1, dtype=torch.int32, device="cuda"), cache.lengths - 1, cache.table,
+                      *cache.codes, *cache.scale)
+    Q = queries(64, B, H * G, D)
+    for sign in (1.0, -1.0):
+        Q[:, :, 5] = sign
+        O = i8.int8_attention_decode(Q, *cache.args())
+        assert torch.isnan(O[:, :G]).all()
+        assert torch.isfinite(O[:, G:]).all()
