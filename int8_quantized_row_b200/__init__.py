@@ -337,7 +337,7 @@ def int8_mixed_linear_fused(X, Wq, sW, W16=None, alpha=6.0, bias=None, act="none
         size = so.int8_mixed_linear_wq_workspace_size if W16 is None else so.int8_mixed_linear_workspace_size
         ws, at, nbytes = _workspace(workspace_buf, 0 if workspace_buf is not None else size(T, K, N), d, X)
         _check("int8_mixed_linear_fused", so.int8_mixed_linear_fused(
-            x, T, K, wq, sw, w16, N, alpha, b, ACTIVATIONS[act], r, _at(Y, "Y", d, f16, (T, N)), at, nbytes, handle))
+            x, T, K, wq, sw, w16, N, float(alpha), b, ACTIVATIONS[act], r, _at(Y, "Y", d, f16, (T, N)), at, nbytes, handle))
     return Y
 
 
@@ -539,8 +539,7 @@ def _cache_args(d, Kc, Vc, sK, sV, block_table):
     (table, max_blocks), B."""
     blocks, H, _, D = Kc.shape
     codes, scales = (blocks, H, KV_BLOCK, D), (blocks, H)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have 2 dimensions")
+    _device_of(block_table, "block_table", 2)
     B, wide = block_table.shape
     return ((_at(Kc, "Kc", d, torch.int8, codes), _at(Vc, "Vc", d, torch.int8, codes),
              _at(sK, "sK", d, torch.float32, scales), _at(sV, "sV", d, torch.float32, scales), blocks),
@@ -606,7 +605,7 @@ def int8_attention_decode(Q, Kc, Vc, sK, sV, block_table, lengths, scale=None, O
         ws, at, nbytes = _workspace(workspace_buf, size, d, Q)
         o, ldo = _rows(O, "O", d, torch.float16, shape)
         _check("int8_attention_decode", so.int8_attention_decode(
-            q, ldq, B, Hq, H, D, *cache, *table, n, D ** -0.5 if scale is None else scale, o, ldo, at, nbytes, handle))
+            q, ldq, B, Hq, H, D, *cache, *table, n, D ** -0.5 if scale is None else float(scale), o, ldo, at, nbytes, handle))
     return O
 
 
@@ -632,5 +631,5 @@ def int8_attention_prompt(Q, K, V, cu_q, cu_k=None, scale=None, O=None, stream=N
         O = Q.new_empty((N, Hq, D)) if O is None else O
         o, ldo = _rows(O, "O", d, f16, (N, Hq, D))
         _check("int8_attention_prompt", so.int8_attention_prompt(
-            q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, D ** -0.5 if scale is None else scale, o, ldo, handle))
+            q, ldq, k, ldk, v, ldv, N, M, Hq, H, D, cq, ck, B, D ** -0.5 if scale is None else float(scale), o, ldo, handle))
     return O

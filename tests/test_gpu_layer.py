@@ -305,3 +305,27 @@ def test_scales_of_a_layer_in_a_stacked_tensor():
         assert all(torch.equal(a, b) for a, b in zip(out, outs[0]))
     assert (scale[0][:, 2] == 7.0).all() and (scale[1][:, 2] == 7.0).all()      # the block that no sequence has
     assert device_status_clean()
+
+
+def test_plain_numbers_of_any_kind_and_tables_that_are_no_tensors():
+    """alpha and scale may be whatever float() takes, as in the older calls; a table that is no CUDA tensor is named."""
+    x, w = torch.randn(4, 256, device="cuda").half(), torch.randn(256, 256, device="cuda").half()
+    Wq, sW = i8.int8_quantize_weight_colwise(w)
+    codes = [torch.randint(-127, 128, (2, 1, 64, 64), dtype=torch.int8, device="cuda") for _ in range(2)]
+    scale = [torch.ones(2, 1, device="cuda") for _ in range(2)]
+    table, length = torch.ones(1, 1, dtype=torch.int32, device="cuda"), torch.full((1,), 50, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 1, 64, device="cuda").half()
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    calls = [lambda v: i8.int8_mixed_linear_fused(x, Wq, sW, w, alpha=v),
+             lambda v: i8.int8_attention_decode(q, *codes, *scale, table, length, scale=v),
+             lambda v: i8.int8_attention_prompt(q, q, q, cu, scale=v)]
+    for call in calls:
+        want = call(2.0)
+        for number in (2, np.float32(2), np.float64(2), torch.tensor(2.0)):
+            assert torch.equal(call(number), want)
+    for bad in (None, [[1]], table.cpu(), table.cpu().numpy()):
+        with pytest.raises(TypeError, match="block_table"):
+            i8.int8_attention_decode(q, *codes, *scale, bad, length)
+        with pytest.raises(TypeError, match="block_table"):
+            i8.int8_kv_append(q, q, cu, length, bad, *codes, *scale)
+    assert device_status_clean()
