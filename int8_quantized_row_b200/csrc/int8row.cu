@@ -1270,9 +1270,12 @@ i8r_status int8_kv_append(const void *K, long long ldk, const void *V, long long
     const dim3 grid(static_cast<unsigned>(items), heads);
     const dim3 block(32 * kv::WARPS);
     // Four warps that keep a whole block in registers among them suit prompts (one
-    // read of the rows: 59 us for 4096 tokens of 96 heads), with two jobs each for one
-    // search (one: 65 us, four: 61, eight: 70); for up to eight rows a sequence a warp
-    // a block does (16 tokens: 8 to 10 us).
+    // read of the rows: 59 us for 4096 tokens of 96 heads, 106 with one warp a block), with
+    // two jobs each for one search (one: 65 us, four: 61, eight: 70); for up to eight rows a
+    // sequence a warp a block does (96 heads, 16 tokens: 8 us for 14 with teams of four; 64
+    // sequences of eight tokens 20 for 45).  The host knows the mean only, and a batch that
+    // mixes prompts with many single tokens pays for it: 63 single tokens and 449 in one
+    // sequence 80 us, for 47 with teams.
     auto launch = [&](auto kernel) { kernel<<<grid, block, 0, stream>>>(p); };
     const bool many = B > 128;
     if (D == 128 && few)
