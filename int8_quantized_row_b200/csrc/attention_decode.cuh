@@ -113,7 +113,7 @@ __device__ __forceinline__ uint32_t weights2(float a, float b) {
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-constexpr float RAISED = 14.0f;          // log2 of what stands in front of the weights
+constexpr float DECODE_RAISED = 14.0f;          // log2 of what stands in front of the weights
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -351,7 +351,7 @@ __device__ __forceinline__ void issue_q(const DecodeParams &p, const Place &w, u
     }
 }
 
-// One piece of an item in memory: per query its maximum - RAISED (log2 units), its sum
+// One piece of an item in memory: per query its maximum - DECODE_RAISED (log2 units), its sum
 // and its D unnormalised values.
 template <int D>
 __device__ __forceinline__ float *piece_row(float *piece, int q) { return piece + q * (D + 2); }
@@ -359,7 +359,7 @@ __device__ __forceinline__ float *piece_row(float *piece, int q) { return piece 
 template <int D, int NT>
 struct State {
     float acc[D / 16][NT][4];            // in units of vs
-    float m[NT][2], l[NT][2];            // maximum - RAISED (log2 units) and sum of this lane's queries 2t, 2t + 1: the same in all its g
+    float m[NT][2], l[NT][2];            // maximum - DECODE_RAISED (log2 units) and sum of this lane's queries 2t, 2t + 1: the same in all its g
     float vs;                            // the scale acc is in (sV/127 of the last block with any)
     uint2 q[D / 16][NT];                 // the queries' fragments
 
@@ -470,7 +470,7 @@ struct State {
                 }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const float to = fmaxf(fmaf(top, ks, -RAISED), m[n][e]);
+                const float to = fmaxf(fmaf(top, ks, -DECODE_RAISED), m[n][e]);
                 alpha[e] = ex2(m[n][e] - to);
                 m[n][e] = to;
 #pragma unroll

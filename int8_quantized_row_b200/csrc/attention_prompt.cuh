@@ -59,11 +59,8 @@ constexpr int PROMPT_THREADS = 384;            // 8 softmax warps and four other
 constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * 128 <= PROMPT_LAUNCH_REGS * PROMPT_THREADS, "more registers than launched with");
 constexpr uint32_t PROMPT_TMEM = 512;
+constexpr float PROMPT_RAISED = 7.0f;                 // log2 of a weight at its row's reference
 constexpr float RAISE = 8.0f;                  // log2 of how far a row may exceed its reference
-// log2 of what stands in front of the weights of a row with this reference (in log2
-// units).  From 2^22 on fp32 rounds a score by 2^-2 and more, which fp16 has no room for
-// beside 2^7 and 2^8.
-__device__ __forceinline__ float raised(float reference) { return fabsf(reference) < 4194304.0f ? 7.0f : 0.0f; }
 
 constexpr int OUT_BYTES = 32 * 128;            // a softmax warp's rows on their way out, 64 columns at a time
 
@@ -573,7 +570,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
         const int i = warp >> 2, quad = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_s = tmem + lanes + i * PT, t_o = tmem + lanes + 2 * PT + i * D;
-        const float sl2 = p.scale_log2, raise = RAISE / sl2;
+        const float sl2 = p.scale_log2;
         int tile = 0, done = 0;                                 // tiles of the ring, steps of this tile before this work
         int turns = 0;                                          // steps of both tiles before this work
         bool ok = true;
@@ -582,7 +579,10 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             const int steps = w.steps[i], cut0 = first_cut(w.seen), cut = first_cut(w.seen + place_of(i, n));
             const int lim = w.seen + place_of(i, n) + quad * 32 + lane;     // the last key the row sees
             const int both = min(w.steps[0], w.steps[1]);
-            float m = -INFINITY, l = 0.0f;
+            // p = 2^(x * sl2 + ref): ref is PROMPT_RAISED - reference (log2 units), infinite before the first
+            // key.  Whether a row has outgrown it is asked of the largest p's own exponent, rounded as
+            // it will be, so that no p exceeds 2^(PROMPT_RAISED + RAISE) however large the scores are.
+            float ref = INFINITY, l = 0.0f;
             for (int j = 0; j < steps; ++j) {
                 ok = ready(&bars->s_full[i], (done + j) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                 if (!ok) break;
@@ -605,11 +605,12 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) top[c] = max3(top[c], x(e + 2 * c), x(e + 2 * c + 1));
                 const float mx = fmaxf(max3(max3(top[0], top[1], x(PT - 4)), max3(top[2], top[3], x(PT - 3)), x(PT - 2)), x(PT - 1));
-                if (__any_sync(0xFFFFFFFFu, mx > m + raise)) {
-                    const float to = fmaxf(m, mx);
-                    const float alpha = m == -INFINITY ? 0.0f : ex2(fmaf(m - to, sl2, raised(to * sl2) - raised(m * sl2)));
+                const float most = fmaf(mx, sl2, ref);          // (NaN where nothing was seen, now or before)
+                if (__any_sync(0xFFFFFFFFu, most > PROMPT_RAISED + RAISE)) {
+                    const float to = most > PROMPT_RAISED ? fmaf(-mx, sl2, PROMPT_RAISED) : ref;
+                    const float alpha = most > PROMPT_RAISED ? ex2(to - ref) : 1.0f;
                     l *= alpha;
-                    m = to;
+                    ref = to;
                     if (j > 0) {
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
@@ -630,9 +631,9 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
                 if (before >= 0 && before < both)
                     ok = ready(&bars->turn[1 - i][quad], (turns + before) & 1, abort, I8R_DEV_TMEM_TIMEOUT);
                 if (!ok) break;
-                // p = 2^(x * scale_log2 - m * scale_log2 + 7); a row that has seen nothing yet has all -inf
-                const float ref = m == -INFINITY ? 0.0f : fmaf(-m, sl2, raised(m * sl2));
-                const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(ref, ref);
+                // (a row that has seen nothing yet has all -inf)
+                const float add = ref == INFINITY ? 0.0f : ref;
+                const uint64_t sl22 = pack2(sl2, sl2), ref2 = pack2(add, add);
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
