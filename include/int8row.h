@@ -362,7 +362,8 @@ i8r_status int8_kv_gather(const int8_t *Kc, const int8_t *Vc, const float *sK, c
  *   O[b,q,:] = sum_t softmax_t( scale * Q[b,q,:] . K[t,:] ) V[t,:],  t < lengths[b]
  * with K and V the values the cache's codes stand for, key/value head
  * h = q / (Hq / H), fp32 scores and sums, and the softmax's weights rounded to
- * fp16 for the product with V.
+ * fp16 for the product with V (by 2^-11 of themselves, and below 2^-28 of the
+ * largest by 2^-39 of that).
  *
  *   Q, O     [B, Hq, D] fp16: head q of sequence b starts at element b*ld + q*D
  *            (ldq, ldo >= Hq*D, multiples of 8); O must not overlap the inputs
@@ -399,7 +400,8 @@ i8r_status int8_attention_decode(const void *Q, long long ldq, int B, int Hq, in
  *   from before the queries, e.g. out of int8_kv_gather):
  *   O[i,q,:] = sum_k softmax_k( scale * Q[i,q,:] . K[k,h,:] ) V[k,h,:],  h = q / (Hq / H)
  * with fp32 scores and sums, and the softmax's weights rounded to fp16 for the
- * product with V.  A row that sees no key (nk < nq) is zeros.
+ * product with V (by 2^-11 of themselves, and below 2^-21 of the largest by 2^-32
+ * of that).  A row that sees no key (nk < nq) is zeros.
  *
  *   Q, O   [N, Hq, D], K, V [M, H, D] fp16: head q of row i starts at element
  *          i*ld + q*D (every ld at least its heads times D and a multiple of 8),

@@ -18,26 +18,28 @@
 // block's K.  With 12 warps that is 48 to 96 KB on the way to every SM.  A lane's
 // bytes are its own mma.sync fragments: m16n8k16 with tokens (then V's columns) as
 // the 16 rows and queries as the 8 columns, which suits one to eight queries per
-// head; at one MMA in ten cycles the legacy tensor path is nowhere near a limit
-// (128 rows of a tcgen05 product would be mostly empty).
+// head; at one MMA in ten cycles the legacy tensor path is nowhere near a limit.  (With
+// two columns of queries the accumulators fill the registers and leave two warps a
+// scheduler.  A tcgen05 product of 128 tokens, or 128 columns of V, by 16 queries would
+// keep them in tensor memory; it has not been built.)
 //
-// Measured: 16 sequences of 2048 tokens, 96 heads of 128: 145 us (805 MB, 5.5 TB/s,
-// 85 % of a copy's rate); 16 of 0 to 2048, 15000 tokens in all: 78 us (4.7 TB/s: about
+// Measured: 16 sequences of 2048 tokens, 96 heads of 128: 149 us (805 MB, 5.4 TB/s,
+// 82 % of a copy's rate); 16 of 0 to 2048, 15000 tokens in all: 79 us (4.7 TB/s: about
 // ten of them are the start, the joins and the uneven end); 64 long ones, 12 queries a
-// head: 262 us (4.4 TB/s, bound by instructions); one of 1000 tokens, 40 heads: 12 us.
+// head: 267 us (4.3 TB/s, bound by instructions); one of 1000 tokens, 40 heads: 14 us.
 //
 // What counts besides bytes is instructions, most of them to turn codes into fp16:
 // xor 0x80 and a byte permute against 0x64 make 1024 + (code + 128), exactly, and a
 // subtraction takes the 1152 off again.  (Left in K's operand and taken off the sums
 // instead, it costs fp32 sums of the size of 1152 |sum(Q)|: scores that are 0.001 to
-// 0.003 off where the queries' mean is 3 to 8, and saves nothing: 264 us for 266 on 64
-// long sequences of 12 queries a head.)  p = 2^14 e^(x - max) is rounded to fp16 for
-// the second product (2^-11, as the output will be), and the softmax's sum is that of
-// the rounded p (one more MMA, with ones for V).  With 2^14 in front a weight down to
-// 2^-28 of the largest is a normal number and is rounded by 2^-39 of the largest below
-// that: with the largest at 1, weights below 2^-25 were lost, 131072 of which are 0.4 %
-// of the result.  The sums over V are kept in units of the current block's scale, so the
-// MMAs accumulate in place.
+// 0.003 off where the queries' mean is 3 to 8, and saves little: 143 us for 149 and 263
+// for 267 on the first and third of the calls above.)  p = 2^14 e^(x - max) is rounded
+// to fp16 for the second product (2^-11, as the output will be), and the softmax's sum is
+// that of the rounded p (one more MMA, with ones for V).  With 2^14 in front a weight
+// down to 2^-28 of the largest is a normal number and is rounded by 2^-39 of the largest
+// below that: with the largest at 1, weights below 2^-25 were lost, 131072 of which are
+// 0.4 % of the result.  The sums over V are kept in units of the current block's scale,
+// so the MMAs accumulate in place.
 #pragma once
 
 #include "device_common.cuh"

@@ -37,9 +37,9 @@
 // cycles for a tile's step of 1024), 11 finds the work and looks over V for what a
 // mask must hide.  Every wait is bounded (timeout -> device status word).
 //
-// Measured: 8192 tokens, 40 query and 8 key heads of 128: 550 us, 1250 TFLOP/s (76 %
-// of the dense 16-bit peak); 4 prompts of 1024, 96 heads: 167 us; 12 of 300: 145 us;
-// 200 tokens, 16 heads of 64: 14 us.  A step of both tiles takes about 3150 cycles
+// Measured: 8192 tokens, 40 query and 8 key heads of 128: 556 us, 1237 TFLOP/s (75 %
+// of the dense 16-bit peak); 4 prompts of 1024, 96 heads: 167 to 172 us; 12 of 300: 160
+// to 168 us; 200 tokens, 16 heads of 64: 12 to 14 us.  A step of both tiles takes about 3150 cycles
 // (exponentials 1770 for a tile in its turn, then 1350 until its next scores are
 // there), of 2048 that either pipe needs; a piece adds about 6000 to its steps.
 #pragma once
@@ -59,7 +59,7 @@ constexpr int PROMPT_THREADS = 384;            // 8 softmax warps and four other
 constexpr int PROMPT_LAUNCH_REGS = 168, SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * 128 <= PROMPT_LAUNCH_REGS * PROMPT_THREADS, "more registers than launched with");
 constexpr uint32_t PROMPT_TMEM = 512;
-constexpr float PROMPT_RAISED = 7.0f;                 // log2 of a weight at its row's reference
+constexpr float PROMPT_RAISED = 7.0f;          // log2 of a weight at its row's reference
 constexpr float RAISE = 8.0f;                  // log2 of how far a row may exceed its reference
 
 constexpr int OUT_BYTES = 32 * 128;            // a softmax warp's rows on their way out, 64 columns at a time
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(PROMPT_THREADS, 1)
             // the CTAs there and back; neighbours are the heads of one tile, which share keys and
             // values.  Sequence s has its tile t at level t + before(s), for each of its tiles.
             // Levels that no sequence has a tile at are passed over: a look at all sequences costs
-            // about 0.4 us for each 32 of them (one row on 2^20 keys beside 4000 short prompts: 207 ms
+            // about 0.4 us for each 32 of them (one row on 2^20 keys beside 4000 short prompts: 203 ms
             // with a look at every level down to theirs, 11 with this, which is the long row alone).
             auto span = [&](int s) {                         // its levels [x, y)
                 const int2 q = kv::row_range(p.cu_q, s, p.N), k = kv::row_range(p.cu_k, s, p.M);

@@ -9,8 +9,8 @@
 //
 // Both kernels are bound by HBM for prompts: append reads 2 bytes and writes 1
 // per value, read-back reads 1 and writes 2.  4096 tokens of 96 heads of 128:
-// append 59 us (5.1 TB/s; one warp a block, and the rounding with conversions that
-// run at an eighth of the rate, took 123), read-back 59 us (5.1 TB/s).  Single
+// append 58 us (5.2 TB/s; one warp a block, and the rounding with conversions that
+// run at an eighth of the rate, took 123), read-back 56 us (5.4 TB/s).  Single
 // tokens are bound by latency: 8 to 10 us for 16 sequences, the chain of finding
 // the block, its scale and its rows.
 #pragma once
