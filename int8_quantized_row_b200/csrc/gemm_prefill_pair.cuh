@@ -129,9 +129,7 @@ __device__ __forceinline__ bool walk_schedule(const Params &p, int nob, int clus
 // 1.7 GB in about 173 us), so the residual and Y cross L2 in whole sectors (rows
 // through a 32 x 32 block in shared memory; 16-byte pieces a lane's row at a time
 // cost 20 us for Y and 50 us for the residual), and eight epilogue warps, half of
-// the columns each, keep the conversion out of the way.  13B fc1, Wq only, all in turns
-// on one GPU: plain instance 186 us, bias alone 199 (so this instance costs 13), with
-// gelu 224 (its special functions 25), with the residual too 232 (8).
+// the columns each, keep the conversion out of the way.
 template <bool kS32, bool kEpi>
 __global__ void __launch_bounds__(kEpi ? THREADS_EPI : THREADS, 1)
     gemm_prefill_pair_kernel(const __grid_constant__ CUtensorMap map_xq, const __grid_constant__ CUtensorMap map_wq,
